@@ -539,3 +539,13 @@ def dsmla_sparse_decode_noalloc(q_nope_bf16: torch.Tensor, q_pe_bf16: torch.Tens
         _dev(indices, "indices", (torch.int32,)), T, H, topk, float(sm_scale),
         _dev(out, "out", _BF16), _dev(lse, "lse", _F32), _stream(stream))
     _check(rc, "dsmla_sparse_decode_noalloc")
+
+
+# the calls of libdsix_prep (they use the checks above)
+from .prep import (PREP_LIB_PATH, ix_layer_norm, ix_layer_norm_bwd, ix_layer_norm_bwd_workspace_size,  # noqa: E402
+                   ix_norm_rope_write_k, ix_plan_step, ix_prep_device_status, ix_rope, ix_rope_frequencies,
+                   ix_rope_table, load_prep)
+
+__all__ += ["PREP_LIB_PATH", "ix_layer_norm", "ix_layer_norm_bwd", "ix_layer_norm_bwd_workspace_size",
+            "ix_norm_rope_write_k", "ix_plan_step", "ix_prep_device_status", "ix_rope", "ix_rope_frequencies",
+            "ix_rope_table", "load_prep"]

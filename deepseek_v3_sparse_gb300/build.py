@@ -1,9 +1,10 @@
-"""Build libdsix.so (the CUDA library behind include/dsix.h) in-tree.
+"""Build libdsix.so (the CUDA library behind include/dsix.h) and libdsix_prep.so
+(include/dsix_prep.h) in-tree.
 
-Every translation unit under csrc/ is compiled for sm_103a only
-(``-gencode arch=compute_103a,code=sm_103a``), in parallel, then linked into
-``deepseek_v3_sparse_gb300/libdsix.so`` with the CUDA runtime linked
-statically.  No cmake; a rebuild is skipped when the library is newer than
+Every translation unit under csrc/ (libdsix) and csrc/prep/ (libdsix_prep) is
+compiled for sm_103a only (``-gencode arch=compute_103a,code=sm_103a``), in
+parallel, then linked into ``deepseek_v3_sparse_gb300/`` with the CUDA runtime
+linked statically.  No cmake; a rebuild is skipped when a library is newer than
 every source.
 """
 from __future__ import annotations
@@ -18,6 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdsix.so")
+OUT_PREP = os.path.join(HERE, "libdsix_prep.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,31 +34,38 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the dsix CUDA library cannot be built")
 
 
-def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+# library -> the folder of its translation units
+LIBRARIES = {OUT: CSRC, OUT_PREP: os.path.join(CSRC, "prep")}
 
 
-def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(ROOT, "include", "dsix.h"), __file__]
+def _sources(out: str = OUT):
+    return sorted(glob.glob(os.path.join(LIBRARIES[out], "*.cu")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(OUT):
+def _deps(out: str = OUT):
+    folders = {CSRC, LIBRARIES[out]}
+    return _sources(out) + [h for d in sorted(folders) for h in glob.glob(os.path.join(d, "*.cuh"))] + \
+        glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__]
+
+
+def up_to_date(out: str = OUT) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(OUT)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(p) <= t for p in _deps(out))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """Builds what is out of date; returns libdsix.so's path."""
+    todo = [out for out in LIBRARIES if force or not up_to_date(out)]
+    if not todo:
         return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include")]
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+        obj = os.path.join(BUILD_DIR, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *inc, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
@@ -68,13 +77,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(compile_one, _sources()))
-    tmp = OUT + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, OUT)
+        objs = {out: [ex.submit(compile_one, src) for src in _sources(out)] for out in todo}
+    for out in todo:
+        tmp = out + f".tmp{os.getpid()}"
+        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o.result() for o in objs[out]], "-cudart", "static"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, out)
     return OUT
 
 

@@ -1,0 +1,309 @@
+// plan.cu -- ix_plan_step: block tables, slot maps and row ranges from lengths.
+//
+// Three prefix sums over the requests (new tokens, whole contexts, missing
+// blocks), then one independent piece of arithmetic per row and per new block,
+// which finds its request by a binary search in the sums.  A step plans a few
+// kilobytes to a few tens of megabytes, so what counts is the number of
+// dependent round trips: up to kFusedBatch requests, every CTA forms the sums
+// itself in shared memory (8 bytes a request, from L2) and goes on to its rows
+// at once, in one launch and without a wait between CTAs.  Above that the
+// redundant sums would cost more than a second launch: one CTA writes them, and
+// the rows search them in global memory.
+//
+// The sums saturate at INT32_MAX.  Saturating addition of non-negative numbers
+// is associative (both orders give min(sum, INT32_MAX)), so 32-bit scans in any
+// order give the saturated sum, and a saturated end shows that it happened.
+#include "prep.cuh"
+
+namespace dsix {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kItems = 4;            // requests per thread and pass of the scan
+constexpr int kRows = 4;             // rows per thread: 16-byte stores of the int32 outputs
+constexpr int kFusedBatch = 4096;    // 3 sums of 4097 entries: 48 KB of shared memory
+constexpr uint32_t kMax = 0x7fffffffu;
+
+struct PlanArgs {
+    const int32_t *cached, *fresh;
+    int batch, block_size, shift;  // shift: log2(block_size), -1 if it is no power of two
+    const int32_t* free_blocks;
+    int64_t n_free;
+    int32_t* table;
+    int64_t stride;
+    int width;
+    int32_t *context_lens, *cu_new, *cu_ctx, *cu_blocks;
+    int64_t *slots, *positions;
+    int32_t *row_req, *row_len, *ks, *ke;
+    int64_t rows;
+    int* status;
+};
+
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, kMax); }
+
+struct Sums {
+    uint32_t n, c, b;  // new tokens, context, missing blocks
+    __device__ __forceinline__ Sums operator+(const Sums& o) const {
+        return {add_sat(n, o.n), add_sat(c, o.c), add_sat(b, o.b)};
+    }
+};
+
+__device__ __forceinline__ uint32_t div_block(const PlanArgs& a, uint32_t x) {
+    return a.shift >= 0 ? x >> a.shift : x / static_cast<uint32_t>(a.block_size);
+}
+
+__device__ __forceinline__ uint32_t blocks_of(const PlanArgs& a, uint32_t tokens) {
+    return tokens ? div_block(a, tokens - 1) + 1 : 0;
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums& s, int d) {
+    return {__shfl_up_sync(0xffffffffu, s.n, d), __shfl_up_sync(0xffffffffu, s.c, d),
+            __shfl_up_sync(0xffffffffu, s.b, d)};
+}
+
+// The exclusive sums of all requests into cn, cc, cb (batch + 1 entries each;
+// shared or global); all threads of the CTA.  `write`: also context_lens, and
+// the status bits.
+__device__ void scan_requests(const PlanArgs& a, int32_t* cn, int32_t* cc, int32_t* cb, bool write) {
+    __shared__ Sums s_warp[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums carry{0, 0, 0};
+    bool bad = false;
+    for (int base = 0; base < a.batch; base += kThreads * kItems) {
+        const int b0 = base + threadIdx.x * kItems;
+        Sums item[kItems], sum{0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int b = b0 + i;
+            int c = 0, n = 0;
+            if (b < a.batch) {
+                c = __ldg(a.cached + b);
+                n = __ldg(a.fresh + b);
+            }
+            bad |= c < 0 || n < 0;
+            const uint32_t uc = max(c, 0), un = max(n, 0), all = add_sat(uc, un);
+            bad |= uc + un > kMax;
+            if (write && b < a.batch) a.context_lens[b] = static_cast<int32_t>(all);
+            item[i] = {un, all, blocks_of(a, all) - blocks_of(a, uc)};
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) sum = sum + item[i];
+        Sums inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sums o = shfl_up(inc, d);
+            if (lane >= d) inc = inc + o;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        Sums total{0, 0, 0}, before{0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w == warp) before = total;
+            total = total + s_warp[w];
+        }
+        Sums ex = shfl_up(inc, 1);
+        if (lane == 0) ex = {0, 0, 0};
+        ex = carry + before + ex;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            if (b0 + i < a.batch) {
+                cn[b0 + i] = static_cast<int32_t>(ex.n);
+                cc[b0 + i] = static_cast<int32_t>(ex.c);
+                cb[b0 + i] = static_cast<int32_t>(ex.b);
+            }
+            ex = ex + item[i];
+        }
+        carry = carry + total;
+        __syncthreads();  // s_warp is written again
+    }
+    if (threadIdx.x == 0) {
+        cn[a.batch] = static_cast<int32_t>(carry.n);
+        cc[a.batch] = static_cast<int32_t>(carry.c);
+        cb[a.batch] = static_cast<int32_t>(carry.b);
+        bad |= carry.n == kMax || carry.c == kMax || carry.b == kMax;
+    }
+    if (write && bad) flag(a.status, IX_DEV_BAD_RANGE);
+}
+
+// the last b in [0, batch) with cu[b] <= t (cu[0] = 0 <= t): empty requests are passed over
+__device__ __forceinline__ int find_request(const int32_t* cu, int batch, int32_t t) {
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t free_block(const PlanArgs& a, int64_t k) {
+    if (k < a.n_free) return __ldg(a.free_blocks + k);
+    flag(a.status, IX_DEV_NO_BLOCK);
+    return -1;
+}
+
+// rows and new blocks, from the sums cn, cc, cb
+__device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, const int32_t* cb) {
+    const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t tid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int32_t total = a.batch ? cn[a.batch] : 0;
+    if (tid == 0 && total > a.rows) flag(a.status, IX_DEV_BAD_RANGE);
+    for (int64_t t0 = tid * kRows; t0 < a.rows; t0 += threads * kRows) {
+        int64_t slot[kRows], pos[kRows];
+        int32_t req[kRows], len[kRows], lo[kRows], hi[kRows];
+        int b = 0;
+        int32_t next = -1, start = 0, cached = 0, ctx = 0, have = 0;  // next: the first row behind request b
+        int32_t block_of = -1, block = -1;                             // the block that `block` was read for
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            slot[i] = -1;
+            pos[i] = 0;
+            req[i] = len[i] = lo[i] = hi[i] = 0;
+            const int64_t t = t0 + i;
+            if (t >= total || t >= a.rows) continue;
+            if (t >= next) {
+                if (i == 0 || next < 0) {
+                    b = find_request(cn, a.batch, static_cast<int32_t>(t));
+                } else {
+                    do ++b; while (cn[b + 1] <= t);
+                }
+                start = cn[b];
+                next = cn[b + 1];
+                ctx = cc[b];
+                cached = max(__ldg(a.cached + b), 0);
+                have = static_cast<int32_t>(blocks_of(a, cached));
+                block_of = -1;
+            }
+            const int64_t p = static_cast<int64_t>(cached) + (t - start);
+            if (p >= static_cast<int64_t>(kMax)) continue;  // a context past INT32_MAX: flagged by the scan
+            const int32_t j = static_cast<int32_t>(div_block(a, static_cast<uint32_t>(p)));
+            if (j != block_of) {
+                block_of = j;
+                block = -1;
+                if (j >= a.width) {
+                    flag(a.status, IX_DEV_BAD_RANGE);
+                } else if (j < have) {
+                    block = a.table[b * a.stride + j];
+                    if (block < 0) flag(a.status, IX_DEV_BAD_BLOCK);
+                } else {
+                    block = free_block(a, static_cast<int64_t>(cb[b]) + (j - have));
+                }
+            }
+            if (block >= 0)
+                slot[i] = static_cast<int64_t>(block) * a.block_size +
+                          (p - static_cast<int64_t>(j) * a.block_size);
+            pos[i] = p;
+            req[i] = b;
+            len[i] = static_cast<int32_t>(p + 1);
+            lo[i] = ctx;
+            hi[i] = static_cast<int32_t>(add_sat(ctx, static_cast<uint32_t>(p + 1)));
+        }
+        if (t0 + kRows <= a.rows) {
+            longlong2* s = reinterpret_cast<longlong2*>(a.slots + t0);
+            longlong2* q = reinterpret_cast<longlong2*>(a.positions + t0);
+            s[0] = make_longlong2(slot[0], slot[1]);
+            s[1] = make_longlong2(slot[2], slot[3]);
+            q[0] = make_longlong2(pos[0], pos[1]);
+            q[1] = make_longlong2(pos[2], pos[3]);
+            *reinterpret_cast<int4*>(a.row_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
+            *reinterpret_cast<int4*>(a.row_len + t0) = make_int4(len[0], len[1], len[2], len[3]);
+            *reinterpret_cast<int4*>(a.ks + t0) = make_int4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<int4*>(a.ke + t0) = make_int4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (t0 + i < a.rows) {
+                    a.slots[t0 + i] = slot[i];
+                    a.positions[t0 + i] = pos[i];
+                    a.row_req[t0 + i] = req[i];
+                    a.row_len[t0 + i] = len[i];
+                    a.ks[t0 + i] = lo[i];
+                    a.ke[t0 + i] = hi[i];
+                }
+            }
+        }
+    }
+    // the new blocks' table entries: no row above reads them
+    const int32_t taken = a.batch ? cb[a.batch] : 0;
+    for (int64_t k = tid; k < taken; k += threads) {
+        const int b = find_request(cb, a.batch, static_cast<int32_t>(k));
+        const int64_t j = static_cast<int64_t>(blocks_of(a, max(__ldg(a.cached + b), 0))) + (k - cb[b]);
+        if (j < a.width)
+            a.table[b * a.stride + j] = free_block(a, k);
+        else
+            flag(a.status, IX_DEV_BAD_RANGE);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) plan_fused_kernel(const PlanArgs a) {
+    extern __shared__ int32_t s_sums[];
+    int32_t *cn = s_sums, *cc = cn + a.batch + 1, *cb = cc + a.batch + 1;
+    scan_requests(a, cn, cc, cb, blockIdx.x == 0);
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int b = threadIdx.x; b <= a.batch; b += kThreads) {
+            a.cu_new[b] = cn[b];
+            a.cu_ctx[b] = cc[b];
+            a.cu_blocks[b] = cb[b];
+        }
+    }
+    expand(a, cn, cc, cb);
+}
+
+__global__ void __launch_bounds__(kThreads) plan_scan_kernel(const PlanArgs a) {
+    scan_requests(a, a.cu_new, a.cu_ctx, a.cu_blocks, true);
+}
+
+__global__ void __launch_bounds__(kThreads) plan_expand_kernel(const PlanArgs a) {
+    expand(a, a.cu_new, a.cu_ctx, a.cu_blocks);
+}
+
+}  // namespace
+}  // namespace dsix
+
+using namespace dsix;
+
+extern "C" int ix_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int batch, int block_size,
+                            const int32_t* free_blocks, int64_t n_free, int32_t* block_table, int64_t bt_stride,
+                            int bt_width, int32_t* context_lens, int32_t* cu_new, int32_t* cu_ctx,
+                            int32_t* cu_blocks, int64_t* slot_mapping, int64_t* positions, int32_t* row_req,
+                            int32_t* row_len, int32_t* ks, int32_t* ke, int64_t rows, ix_stream_t stream) {
+    if (batch < 0 || n_free < 0 || bt_stride < 0 || bt_width < 0 || rows < 0 || bt_width > bt_stride)
+        return IX_ERR_SHAPE;
+    if (block_size < 1 || rows > INT32_MAX) return IX_ERR_UNSUPPORTED;
+    if (!cu_new || !cu_ctx || !cu_blocks) return IX_ERR_NULL;
+    if (batch > 0 && (!cached_lens || !new_lens || !context_lens)) return IX_ERR_NULL;
+    if (batch > 0 && bt_width > 0 && !block_table) return IX_ERR_NULL;
+    if (n_free > 0 && !free_blocks) return IX_ERR_NULL;
+    if (rows > 0 && (!slot_mapping || !positions || !row_req || !row_len || !ks || !ke)) return IX_ERR_NULL;
+    if (!aligned_to(cached_lens, 4) || !aligned_to(new_lens, 4) || !aligned_to(free_blocks, 4) ||
+        !aligned_to(block_table, 4) || !aligned_to(context_lens, 4) || !aligned_to(cu_new, 4) ||
+        !aligned_to(cu_ctx, 4) || !aligned_to(cu_blocks, 4) || !aligned16(slot_mapping) || !aligned16(positions) ||
+        !aligned16(row_req) || !aligned16(row_len) || !aligned16(ks) || !aligned16(ke))
+        return IX_ERR_ALIGN;
+    int* st = status_ptr();
+    const int sms = num_sms();
+    if (!st || sms <= 0) return IX_ERR_CUDA;
+    int shift = -1;
+    if ((block_size & (block_size - 1)) == 0) shift = __builtin_ctz(static_cast<unsigned>(block_size));
+    const PlanArgs a{cached_lens, new_lens, batch, block_size, shift, free_blocks, n_free, block_table,
+                     bt_stride, bt_width, context_lens, cu_new, cu_ctx, cu_blocks, slot_mapping, positions,
+                     row_req, row_len, ks, ke, rows, st};
+    const int64_t want = (rows + kThreads * kRows - 1) / (kThreads * kRows);
+    const int grid = static_cast<int>(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (batch <= kFusedBatch) {
+        const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);
+        if (smem > 48 * 1024 - sizeof(Sums) * (kThreads / 32) &&
+            cudaFuncSetAttribute(plan_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 3 * sizeof(int32_t) * (kFusedBatch + 1)) != cudaSuccess)
+            return IX_ERR_CUDA;
+        plan_fused_kernel<<<grid, kThreads, smem, s>>>(a);
+        return launch_status();
+    }
+    plan_scan_kernel<<<1, kThreads, 0, s>>>(a);
+    const int rc = launch_status();
+    if (rc != IX_OK) return rc;
+    plan_expand_kernel<<<grid, kThreads, 0, s>>>(a);
+    return launch_status();
+}

@@ -1,0 +1,222 @@
+/*
+ * dsix_prep.h -- C ABI of libdsix_prep: what a step of the sparse-attention
+ * indexer needs before its logits (dsix.h), on one GB300 (sm_103a):
+ *   ix_plan_step          block tables, slot maps and row ranges from request lengths
+ *   ix_rope_frequencies   the (scaled) rotary frequencies, on the host
+ *   ix_rope_table         the cosine and sine table of those frequencies
+ *   ix_rope               rotary positions of a part of every head, and their gradient
+ *   ix_layer_norm[_bwd]   layer norm and its gradient
+ *   ix_norm_rope_write_k  the indexer key's layer norm, rotary positions, fp8
+ *                         coding and write into the paged cache, in one pass
+ *
+ * The conventions are those of dsix.h: device pointers owned by the caller
+ * unless a comment says otherwise, nothing allocated, nothing synchronised,
+ * every call asynchronous on `stream` and capturable, argument errors returned
+ * before anything is launched, and what only the device can see checked there:
+ * an entry out of range is skipped and ORs an IX_DEV_* bit into this library's
+ * status word (ix_prep_device_status).
+ *
+ * Strides count elements of the tensor's type, are not negative, and the last
+ * dimension is contiguous.  Buffers of one call do not overlap, except where an
+ * output may be its input ("in place").
+ */
+#ifndef DSIX_PREP_H
+#define DSIX_PREP_H
+
+#include "dsix.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Types of activations. */
+enum { IX_BF16 = 0, IX_FP16 = 1, IX_FP32 = 2 };
+
+/* Further bits of the status word (IX_DEV_BAD_SLOT, _BAD_BLOCK, _BAD_RANGE and
+ * _BAD_POSITION of dsix.h are used too). */
+enum {
+    IX_DEV_NO_BLOCK = 128 /* the free list was shorter than the blocks a step needs */
+};
+
+/* ix_rope's flags. */
+enum {
+    IX_ROPE_INTERLEAVED = 1, /* pairs (2i, 2i + 1) instead of (i, i + rot / 2) */
+    IX_ROPE_INVERSE = 2      /* the transposed rotation: the gradient of the forward call */
+};
+
+/* ix_rope_frequencies' scalings. */
+enum { IX_ROPE_PLAIN = 0, IX_ROPE_LINEAR = 1, IX_ROPE_NTK = 2, IX_ROPE_YARN = 3 };
+
+/* As ix_device_status, for the calls of this header.  SYNCHRONOUS. */
+IX_API int ix_prep_device_status(int* status_out);
+
+/*
+ * ix_plan_step -- from the requests' lengths, everything that the calls of a
+ * step index by.  Request b has cached_lens[b] = c tokens in the cache and
+ * brings new_lens[b] = n more (either may be 0); a negative length counts as 0
+ * and sets IX_DEV_BAD_RANGE.
+ *   context_lens[b] = c + n
+ *   cu_new          = exclusive prefix sums of n, batch + 1 entries
+ *   cu_ctx          = exclusive prefix sums of c + n (ix_gather_k's cu_seq_lens)
+ *   cu_blocks       = exclusive prefix sums of the blocks each request still
+ *                     lacks, ceil((c + n) / bs) - ceil(c / bs); its last entry is
+ *                     how many entries of free_blocks the step takes
+ *   block_table[b, ceil(c / bs) + j] = free_blocks[cu_blocks[b] + j]; the entries
+ *                     before (the cached tokens' blocks) are read, all others
+ *                     left as they are
+ * and for the step's rows, request after request, row t with position
+ * p = c + t - cu_new[b]:
+ *   positions[t] = p,  row_req[t] = b,  row_len[t] = p + 1,
+ *   slot_mapping[t] = block_table[b, p / bs] * bs + p % bs,
+ *   ks[t] = cu_ctx[b],  ke[t] = cu_ctx[b] + p + 1   (ix_mqa_logits' ranges)
+ * Rows at or past cu_new[batch] (a step padded to `rows`) get slot -1, which the
+ * cache writes skip, and zeros elsewhere: an empty row.
+ * What does not fit is left out, and a bit is set: rows past `rows`
+ * (IX_DEV_BAD_RANGE), blocks past n_free or past the table's width get table
+ * entry and slots -1 (IX_DEV_NO_BLOCK, IX_DEV_BAD_RANGE), a cached block that is
+ * negative gives slot -1 (IX_DEV_BAD_BLOCK).  Sums are formed in 64 bits; one
+ * above INT32_MAX is written as INT32_MAX and sets IX_DEV_BAD_RANGE.
+ * The call only reads the free list and is repeatable: the same lengths give the
+ * same table.
+ *   cached_lens, new_lens, context_lens  int32 [batch]
+ *   free_blocks  int32 [n_free], block ids in the order they are handed out
+ *   block_table  int32 [batch, bt_stride], of which bt_width columns are used
+ *   cu_new, cu_ctx, cu_blocks  int32 [batch + 1]
+ *   slot_mapping, positions    int64 [rows], 16-byte aligned
+ *   row_req, row_len, ks, ke   int32 [rows], 16-byte aligned
+ * block_size >= 1.  batch == 0 writes the three zero sums and `rows` empty rows.
+ */
+IX_API int ix_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int batch, int block_size,
+                        const int32_t* free_blocks, int64_t n_free, int32_t* block_table, int64_t bt_stride,
+                        int bt_width, int32_t* context_lens, int32_t* cu_new, int32_t* cu_ctx,
+                        int32_t* cu_blocks, int64_t* slot_mapping, int64_t* positions, int32_t* row_req,
+                        int32_t* row_len, int32_t* ks, int32_t* ke, int64_t rows, ix_stream_t stream);
+
+/*
+ * ix_rope_frequencies -- HOST only: inv_freq[i], i < rot / 2, in radians per
+ * position.  With w_i = base^(-2i / rot):
+ *   IX_ROPE_PLAIN   w_i
+ *   IX_ROPE_LINEAR  w_i / factor (positions interpolated)
+ *   IX_ROPE_NTK     w_i of the base base * factor^(rot / (rot - 2)): the slowest
+ *                   pair is stretched by factor, the fastest keeps its frequency
+ *   IX_ROPE_YARN    w_i (1 - g_i) + (w_i / factor) g_i, where g rises from 0 to 1
+ *                   between the pairs that make beta_fast and beta_slow turns
+ *                   over `original` positions: with
+ *                   d(b) = rot ln(original / (2 pi b)) / (2 ln base),
+ *                   low = max(floor(d(beta_fast)), 0), high = min(ceil(d(beta_slow)), rot - 1),
+ *                   g_i = clamp((i - low) / max(high - low, 0.001), 0, 1)
+ * rot even, 2..256; base > 1; factor >= 1 (all but PLAIN); YARN: original > 0,
+ * beta_fast >= beta_slow > 0.  IX_ERR_UNSUPPORTED otherwise.
+ */
+IX_API int ix_rope_frequencies(int scaling, int rot, double base, double factor, double original,
+                               double beta_fast, double beta_slow, double* inv_freq);
+
+/*
+ * ix_rope_table -- rows first .. first + n - 1 of a rotary table, in the layout
+ * that the rotary calls of this header and of dsix.h read:
+ *   cos_sin[r, i] = amplitude * cos((first + r) * inv_freq[i]),
+ *   cos_sin[r, rot / 2 + i] = amplitude * sin(...)
+ * The angle is reduced exactly in 64-bit fixed-point turns (the frequency is
+ * rounded once to 2^-64 turns per position), so far positions cost no accuracy.
+ *   inv_freq  HOST double [rot / 2], finite (read during the call)
+ *   cos_sin   f32 [n, rot], 16-byte aligned
+ * rot even, 2..256; 0 <= first, first + n <= 2^40.
+ */
+IX_API int ix_rope_table(const double* inv_freq, int rot, int64_t first, int64_t n, double amplitude,
+                         float* cos_sin, ix_stream_t stream);
+
+/*
+ * ix_rope -- rotary positions.  For token t, head h and pair i < rot / 2, with
+ * p = positions[t], c = cos_sin[p, i], s = cos_sin[p, rot / 2 + i] (s negated
+ * under IX_ROPE_INVERSE) and the pair (a, b) at offset + i and
+ * offset + rot / 2 + i (IX_ROPE_INTERLEAVED: offset + 2i and offset + 2i + 1) of
+ * x[t, h, :]:
+ *   out[t, h, :] holds (a c - b s, a s + b c) there and x's values elsewhere.
+ * f32 arithmetic, one rounding to the output's type.  The inverse call on an
+ * output's gradient gives the input's gradient.
+ * A second tensor x2 with heads2 heads of the same head_dim and type (keys beside
+ * queries) is turned in the same launch; x2 NULL: none.
+ * out may be x in place (same pointer and strides): only the rotated part is
+ * then read and written.  A position outside [0, max_pos) sets
+ * IX_DEV_BAD_POSITION and the token's outputs are not written.
+ *   x, out      dtype [tokens, heads, head_dim], token and head strides as given
+ *               (an input may be broadcast with stride 0)
+ *   positions   int64 [tokens];  cos_sin  f32 [max_pos, rot], 4-byte aligned
+ * rot even, 2..256, 0 <= offset, offset + rot <= head_dim, heads 1..65536, head_dim <= 65536.
+ * IX_ERR_SHAPE: a negative size or stride, an output whose heads overlap.
+ */
+typedef struct {
+    const void* x;
+    void* out;
+    int heads;
+    int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+} ix_rope_tensor;
+
+IX_API int ix_rope(const ix_rope_tensor* x, const ix_rope_tensor* x2, int dtype, int64_t tokens, int head_dim,
+                   int offset, const int64_t* positions, const float* cos_sin, int64_t max_pos, int rot,
+                   int flags, ix_stream_t stream);
+
+/*
+ * ix_layer_norm -- for every row r of x [rows, cols]:
+ *   mean = sum x / cols,  var = sum (x - mean)^2 / cols,  rstd = 1 / sqrt(var + eps),
+ *   out = (x - mean) * rstd * gamma + beta
+ * in f32, the row held on chip (the squares are those of the centred values),
+ * one rounding to out's type.
+ *   x, out       dtype [rows, cols], row strides as given; out may be x in place
+ *   gamma, beta  [cols] of type weight_dtype (IX_FP32 or dtype), 16-byte aligned;
+ *                either may be NULL (1 and 0)
+ *   mean, rstd   f32 [rows], for the backward pass; both or neither NULL
+ * 1 <= cols <= 32768, eps >= 0 and finite.
+ */
+IX_API int ix_layer_norm(const void* x, int64_t x_stride, const void* gamma, const void* beta, int weight_dtype,
+                         float eps, int64_t rows, int cols, void* out, int64_t out_stride, float* mean,
+                         float* rstd, int dtype, ix_stream_t stream);
+
+/*
+ * ix_layer_norm_bwd -- the gradient of ix_layer_norm.  With
+ * xhat = (x - mean) * rstd and h = dy * gamma:
+ *   dx = rstd * (h - sum h / cols - xhat * sum(h * xhat) / cols)
+ *   dgamma[c] = sum over rows of dy * xhat,  dbeta[c] = sum over rows of dy
+ * The column sums are formed in f32 in an order that depends on the sizes, the
+ * type and the alignment alone: the same call gives the same bits.
+ *   dy, x, dx      dtype [rows, cols], row strides as given; dx may be dy in place
+ *   gamma          as in the forward call (NULL: 1)
+ *   mean, rstd     f32 [rows], the forward call's
+ *   dgamma, dbeta  f32 [cols], overwritten; both or neither NULL
+ *   workspace      of at least ix_layer_norm_bwd_workspace_size(rows, cols) bytes,
+ *                  16-byte aligned, any contents; not needed without dgamma
+ */
+IX_API size_t ix_layer_norm_bwd_workspace_size(int64_t rows, int cols);
+IX_API int ix_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* gamma,
+                             int weight_dtype, const float* mean, const float* rstd, int64_t rows, int cols,
+                             void* dx, int64_t dx_stride, float* dgamma, float* dbeta, int dtype,
+                             void* workspace, size_t workspace_bytes, ix_stream_t stream);
+
+/*
+ * ix_norm_rope_write_k -- the indexer key from its projection to the paged
+ * cache.  For every token t with slot = slot_mapping[t] >= 0, in f32 throughout:
+ *   y     = layer norm of k[t, :] with gamma, beta and eps (ix_layer_norm)
+ *   z     = y with rot values from `offset` on turned by positions[t] (ix_rope)
+ *   scale = max(amax |z| / 448, FLT_MIN),  v[i] = fp8(z[i] / scale)
+ * written as ix_quant_write_k writes its key.  y and z are not rounded on the
+ * way.  Tokens with a negative slot are skipped; a slot past the pool sets
+ * IX_DEV_BAD_SLOT, a position outside [0, max_pos) IX_DEV_BAD_POSITION, and the
+ * token is skipped.
+ *   k            dtype [n, 128], row stride as given; rows 16-byte aligned
+ *   gamma, beta  f32 [128], 16-byte aligned
+ *   positions, slot_mapping  int64 [n];  cos_sin  f32 [max_pos, rot], 16-byte aligned
+ *   cache        uint8 [num_blocks, 64 * 132], 16-byte aligned
+ * rot 16, 32, 64, 96 or 128; offset a multiple of 16, offset + rot <= 128;
+ * block_size 64; eps >= 0 and finite.
+ */
+IX_API int ix_norm_rope_write_k(const void* k, int64_t k_stride, int dtype, int64_t n, const float* gamma,
+                                const float* beta, float eps, const int64_t* positions, const float* cos_sin,
+                                int64_t max_pos, int rot, int offset, int interleaved,
+                                const int64_t* slot_mapping, uint8_t* cache, int64_t num_blocks, int block_size,
+                                ix_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DSIX_PREP_H */
