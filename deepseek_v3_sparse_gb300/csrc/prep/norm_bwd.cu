@@ -2,16 +2,14 @@
 //
 // One pass over dy and x gives dx and the column sums: a thread holds the same
 // columns of every row it takes, so it adds up their dy * xhat and dy in
-// registers.  At most kParts CTAs walk the rows; each writes its sums once, and
-// a second kernel adds those in the order of the CTAs (the bits do not depend on
-// which CTA ends first).  Rows too wide for a thread's registers to hold the sums
-// beside the row take their column sums in a pass of their own.
+// registers.  The CTAs that walk the rows write their sums once, and a second
+// kernel adds those in the order of the CTAs (the bits do not depend on which CTA
+// ends first).  Rows too wide for a thread's registers to hold the sums beside
+// the row take their column sums in a pass of their own.
 #include "norm.cuh"
 
 namespace dsix {
 namespace {
-
-constexpr int kParts = 304;  // two CTAs on each of 152 SMs
 
 struct BwdArgs {
     const void *dy, *x, *gamma;
@@ -23,88 +21,121 @@ struct BwdArgs {
     float inv_cols;
 };
 
+// CTAs that write column sums, at most: what their sums cost is bounded, also
+// where the columns are many
+constexpr int max_parts(int cols) { return kSms * (cols <= 2048 ? 4 : cols <= 4096 ? 3 : 2); }
+
 template <class T, int V, int G, int U, bool kSums>
-__global__ void __launch_bounds__(RowShape<G>::threads) norm_bwd_kernel(const BwdArgs a) {
-    using S = RowShape<G>;
-    __shared__ float s_sum[4][32];
-    const int t = threadIdx.x % G;
-    float ag[kSums ? U * V : 1], ab[kSums ? U * V : 1];
-    if constexpr (kSums) {
-#pragma unroll
-        for (int i = 0; i < U * V; ++i) ag[i] = ab[i] = 0.f;
-    }
-    int flip = 0;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * S::rows; r0 < a.rows;
-         r0 += static_cast<int64_t>(gridDim.x) * S::rows) {
-        const int64_t row = r0 + threadIdx.x / G;
-        const bool live = row < a.rows;
+struct Bwd : RowShape<G> {
+    static constexpr int E = U * V, words = U * ((V * sizeof(T) + 3) / 4);
+    static constexpr bool hold = E <= 16 && V > 1 && G < 1024;
+    static constexpr int ahead = RowShape<G>::narrow && words <= 4 ? 2 : E <= 16 ? 1 : 0;
+    // the same shape with and without the column sums
+    static constexpr int ctas =
+        ctas_per_sm(RowShape<G>::threads, 2 * E + (hold ? E : 0) + (ahead + 1) * 2 * words + 32);
+};
+
+template <class T, int V, int G, int U, bool kSums>
+__global__ void __launch_bounds__(Bwd<T, V, G, U, kSums>::threads, Bwd<T, V, G, U, kSums>::ctas)
+    norm_bwd_kernel(const BwdArgs a) {
+    using F = Bwd<T, V, G, U, kSums>;
+    __shared__ float s_sum[2][2][32];
+    const int t = threadIdx.x % G, sub = threadIdx.x / G;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * F::rows;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * F::rows;
+    struct Row {
         Vec<T, V> x[U], dy[U];
+        float mean, rstd;
+    };
+    // a row past the end has dy = x = 0 and mean = rstd = 0: it adds nothing
+    auto load = [&](Row& r, int64_t row) {
+        const bool live = row < a.rows;
         const T* px = static_cast<const T*>(a.x) + row * a.x_stride;
         const T* pd = static_cast<const T*>(a.dy) + row * a.dy_stride;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (u * G + t) * V;
-            if (live && c < a.cols) {
-                x[u] = load_vec<T, V>(px + c);
-                dy[u] = load_vec<T, V>(pd + c);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[u].v[i] = dy[u].v[i] = from_f32<T>(0.f);
-            }
+            r.x[u] = live && c < a.cols ? load_vec<T, V>(px + c) : zero_vec<T, V>();
+            r.dy[u] = live && c < a.cols ? load_vec<T, V>(pd + c) : zero_vec<T, V>();
         }
-        const float mean = live ? __ldg(a.mean + row) : 0.f, rstd = live ? __ldg(a.rstd + row) : 0.f;
-        float sh = 0.f, shx = 0.f;
+        r.mean = live ? __ldg(a.mean + row) : 0.f;
+        r.rstd = live ? __ldg(a.rstd + row) : 0.f;
+    };
+    auto weight = [&](float(&w)[V], int c) {
+        fill<V>(w, 1.f);
+        if (a.gamma && c < a.cols) load_weight<T, V>(a.gamma, a.weight_f32, c, w);
+    };
+    Row ring[F::ahead + 1];
+#pragma unroll
+    for (int k = 0; k <= F::ahead; ++k) load(ring[k], row0 + k * step + sub);
+    float ag[kSums ? F::E : 1], ab[kSums ? F::E : 1], g[F::hold ? U : 1][V];
+    if constexpr (kSums) {
+        fill<F::E>(ag, 0.f);
+        fill<F::E>(ab, 0.f);
+    }
+    if constexpr (F::hold) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) weight(g[u], (u * G + t) * V);
+    }
+    int flip = 0;  // the sums of consecutive rows use other places: one barrier a row is enough
+    for (int64_t r0 = row0; r0 < a.rows; r0 += step) {
+        const Row& r = ring[0];
+        const int64_t row = r0 + sub;
+        float sums[2] = {0.f, 0.f};  // of h and h * xhat
+        // roundings spelled out: with and without the column sums, dx has the same bits
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = (u * G + t) * V;
+            if constexpr (!F::hold) weight(g[0], c);
             if (c < a.cols) {
-                float g[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = 1.f;
-                if (a.gamma) load_weight<T, V>(a.gamma, a.weight_f32, c, g);
+                float x[V], d[V];
+                r.x[u].unpack(x);
+                r.dy[u].unpack(d);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    // roundings spelled out: with and without the column sums, dx has the same bits
-                    const float d = to_f32(dy[u].v[i]), h = __fmul_rn(d, g[i]);
-                    const float xh = __fmul_rn(__fsub_rn(to_f32(x[u].v[i]), mean), rstd);
-                    sh = __fadd_rn(sh, h);
-                    shx = fmaf(h, xh, shx);
+                    const float xh = __fmul_rn(__fsub_rn(x[i], r.mean), r.rstd);
+                    const float h = __fmul_rn(d[i], g[F::hold ? u : 0][i]);
+                    sums[0] = __fadd_rn(sums[0], h);
+                    sums[1] = fmaf(h, xh, sums[1]);
                     if constexpr (kSums) {
-                        // a row past the end has dy = 0, mean = rstd = 0: it adds nothing
-                        ag[u * V + i] = fmaf(d, xh, ag[u * V + i]);
-                        ab[u * V + i] += d;
+                        ag[u * V + i] = fmaf(d[i], xh, ag[u * V + i]);
+                        ab[u * V + i] += d[i];
                     }
                 }
             }
         }
-        // the sums of consecutive rows use other places, so one barrier a sum is enough
-        const float mh = __fmul_rn(row_sum<G>(sh, s_sum[2 * flip]), a.inv_cols);
-        const float mhx = __fmul_rn(row_sum<G>(shx, s_sum[2 * flip + 1]), a.inv_cols);
+        row_sums<G>(sums, s_sum[flip]);
         flip ^= 1;
-        if (!live) continue;
-        T* out = static_cast<T*>(a.dx) + row * a.dx_stride;
+        if (row < a.rows) {
+            const float mh = __fmul_rn(sums[0], a.inv_cols), mhx = __fmul_rn(sums[1], a.inv_cols);
+            T* out = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (u * G + t) * V;
-            if (c < a.cols) {
-                float g[V];
+            for (int u = 0; u < U; ++u) {
+                const int c = (u * G + t) * V;
+                if constexpr (!F::hold) weight(g[0], c);
+                if (c < a.cols) {
+                    float x[V], d[V];
+                    r.x[u].unpack(x);
+                    r.dy[u].unpack(d);
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = 1.f;
-                if (a.gamma) load_weight<T, V>(a.gamma, a.weight_f32, c, g);
-                Vec<T, V> y;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = __fmul_rn(__fsub_rn(to_f32(x[u].v[i]), mean), rstd);
-                    const float h = __fmul_rn(to_f32(dy[u].v[i]), g[i]);
-                    y.v[i] = from_f32<T>(__fmul_rn(rstd, fmaf(-xh, mhx, __fsub_rn(h, mh))));
+                    for (int i = 0; i < V; ++i) {
+                        const float xh = __fmul_rn(__fsub_rn(x[i], r.mean), r.rstd);
+                        const float h = __fmul_rn(d[i], g[F::hold ? u : 0][i]);
+                        d[i] = __fmul_rn(r.rstd, fmaf(-xh, mhx, __fsub_rn(h, mh)));
+                    }
+                    Vec<T, V> y;
+                    y.pack(d);
+                    store_vec<T, V>(out + c, y);
                 }
-                store_vec<T, V>(out + c, y);
             }
         }
+#pragma unroll
+        for (int k = 0; k < F::ahead; ++k) ring[k] = ring[k + 1];
+        load(ring[F::ahead], row + (F::ahead + 1) * step);
     }
     if constexpr (kSums) {
         float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-        if constexpr (!S::narrow) {
+        if constexpr (!F::narrow) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -117,7 +148,7 @@ __global__ void __launch_bounds__(RowShape<G>::threads) norm_bwd_kernel(const Bw
                 }
         } else {
             // the CTA's row groups: those of a warp by shuffles, the warps in shared memory
-            constexpr int kWarps = S::threads / 32, kCols = G * U * V;
+            constexpr int kWarps = F::threads / 32, kCols = G * U * V;
             __shared__ float s_part[kWarps][kCols];
             const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 #pragma unroll
@@ -133,7 +164,7 @@ __global__ void __launch_bounds__(RowShape<G>::threads) norm_bwd_kernel(const Bw
                         if (lane < G) s_part[warp][(u * G + t) * V + i] = v;
                     }
                 __syncthreads();
-                for (int c = threadIdx.x; c < a.cols; c += S::threads) {
+                for (int c = threadIdx.x; c < a.cols; c += F::threads) {
                     float v = 0.f;
 #pragma unroll
                     for (int k = 0; k < kWarps; ++k) v += s_part[k][c];
@@ -190,11 +221,12 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int
 
 template <class T, int V, int G, int U, bool kSums>
 int launch(const BwdArgs& a, int* parts, cudaStream_t s) {
-    constexpr int R = RowShape<G>::rows;
-    const int64_t want = (a.rows + R - 1) / R;
-    const int grid = static_cast<int>(want < kParts ? want : kParts);
+    using F = Bwd<T, V, G, U, kSums>;
+    const int64_t want = (a.rows + F::rows - 1) / F::rows;
+    const int cap = max_parts(a.cols), most = kSms * F::ctas < cap ? kSms * F::ctas : cap;
+    const int grid = static_cast<int>(want < most ? want : most);
     if (kSums) *parts = grid;
-    norm_bwd_kernel<T, V, G, U, kSums><<<grid, RowShape<G>::threads, 0, s>>>(a);
+    norm_bwd_kernel<T, V, G, U, kSums><<<grid, F::threads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -206,7 +238,7 @@ int fused(const BwdArgs& a, bool wide, int* parts, cudaStream_t s) {
         if (n <= 16) return launch<T, W, 16, 1, kSums>(a, parts, s);
         if (n <= 32) return launch<T, W, 32, 1, kSums>(a, parts, s);
         if (n <= 64) return launch<T, W, 32, 2, kSums>(a, parts, s);
-        if (n <= 256) return launch<T, W, 128, 2, kSums>(a, parts, s);
+        if (n <= 256) return launch<T, W, 256, 1, kSums>(a, parts, s);
         if (n <= 512) return launch<T, W, 256, 2, kSums>(a, parts, s);
         if (n <= 1024) return launch<T, W, 512, 2, kSums>(a, parts, s);
         if (n <= 2048) return launch<T, W, 512, 4, kSums>(a, parts, s);
@@ -219,8 +251,8 @@ int fused(const BwdArgs& a, bool wide, int* parts, cudaStream_t s) {
     const int n = a.cols;
     if (n <= 32) return launch<T, 1, 32, 1, kSums>(a, parts, s);
     if (n <= 128) return launch<T, 1, 32, 4, kSums>(a, parts, s);
-    if (n <= 512) return launch<T, 1, 32, 16, kSums>(a, parts, s);
-    if (n <= 2048) return launch<T, 1, 128, 16, kSums>(a, parts, s);
+    if (n <= 512) return launch<T, 1, 128, 4, kSums>(a, parts, s);
+    if (n <= 2048) return launch<T, 1, 256, 8, kSums>(a, parts, s);
     if (n <= 8192) return launch<T, 1, 512, 16, kSums>(a, parts, s);
     if constexpr (!kSums) return launch<T, 1, 1024, 32, false>(a, parts, s);
     return IX_ERR_UNSUPPORTED;
@@ -238,7 +270,7 @@ int dispatch(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
             rc = fused<T, true>(a, wide, &parts, s);
         } else {
             // before dx is written: dx may be dy in place
-            parts = static_cast<int>(a.rows < kParts ? a.rows : kParts);
+            parts = static_cast<int>(a.rows < max_parts(a.cols) ? a.rows : max_parts(a.cols));
             norm_cols_kernel<T><<<dim3((a.cols + kColThreads - 1) / kColThreads, parts), kColThreads, 0, s>>>(a);
             rc = launch_status();
             if (rc == IX_OK) rc = fused<T, false>(a, wide, nullptr, s);
@@ -257,7 +289,8 @@ using namespace dsix;
 
 extern "C" size_t ix_layer_norm_bwd_workspace_size(int64_t rows, int cols) {
     if (rows <= 0 || cols <= 0) return 0;
-    return static_cast<size_t>(rows < kParts ? rows : kParts) * 2 * static_cast<size_t>(cols) * sizeof(float);
+    const int most = max_parts(cols);
+    return static_cast<size_t>(rows < most ? rows : most) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 
 extern "C" int ix_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

@@ -19,72 +19,108 @@ struct NormArgs {
 };
 
 template <class T, int V, int G, int U>
-__global__ void __launch_bounds__(RowShape<G>::threads) norm_fwd_kernel(const NormArgs a) {
-    __shared__ float s_sum[2][32];
+struct Fwd : RowShape<G> {
+    static constexpr int E = U * V, words = U * ((V * sizeof(T) + 3) / 4);
+    // the weights stay in registers where a thread has few columns
+    static constexpr bool hold = E <= 16 && V > 1 && G < 1024;
+    static constexpr int ahead = RowShape<G>::narrow && words <= 4 ? 3 : E <= 16 ? 1 : 0;
+    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, (hold ? 2 * E : 0) + (ahead + 1) * words + 36);
+};
+
+template <class T, int V, int G, int U>
+__global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::ctas) norm_fwd_kernel(const NormArgs a) {
+    using F = Fwd<T, V, G, U>;
+    __shared__ float s_sum[4][1][32];
     const int t = threadIdx.x % G;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * RowShape<G>::rows + threadIdx.x / G;
-    const bool live = row < a.rows;
-    Vec<T, V> x[U];
-    const T* in = static_cast<const T*>(a.x) + row * a.x_stride;
-    float sum = 0.f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * F::rows;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * F::rows;
+    const int sub = threadIdx.x / G;
+    auto load = [&](Vec<T, V>(&x)[U], int64_t row) {
+        const T* in = static_cast<const T*>(a.x) + row * a.x_stride;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = (u * G + t) * V;
-        if (live && c < a.cols) {
-            x[u] = load_vec<T, V>(in + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[u].v[i] = from_f32<T>(0.f);
+        for (int u = 0; u < U; ++u) {
+            const int c = (u * G + t) * V;
+            x[u] = row < a.rows && c < a.cols ? load_vec<T, V>(in + c) : zero_vec<T, V>();
         }
-    }
+    };
+    Vec<T, V> ring[F::ahead + 1][U];  // the present row and the next ones
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += to_f32(x[u].v[i]);
-    const float mean = row_sum<G>(sum, s_sum[0]) * a.inv_cols;
-    float sq = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if ((u * G + t) * V < a.cols) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = to_f32(x[u].v[i]) - mean;
-                sq = fmaf(d, d, sq);
-            }
-        }
-    }
-    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(row_sum<G>(sq, s_sum[1]), a.inv_cols, a.eps)));
-    if (!live) return;
-    if (t == 0 && a.mean) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
-    }
-    T* out = static_cast<T*>(a.out) + row * a.out_stride;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = (u * G + t) * V;
+    for (int k = 0; k <= F::ahead; ++k) load(ring[k], row0 + k * step + sub);
+    float g[F::hold ? U : 1][V], b[F::hold ? U : 1][V];
+    auto weights = [&](float(&gv)[V], float(&bv)[V], int c) {
+        fill<V>(gv, 1.f);
+        fill<V>(bv, 0.f);
         if (c < a.cols) {
-            float g[V], b[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g[i] = 1.f;
-                b[i] = 0.f;
-            }
-            if (a.gamma) load_weight<T, V>(a.gamma, a.weight_f32, c, g);
-            if (a.beta) load_weight<T, V>(a.beta, a.weight_f32, c, b);
-            Vec<T, V> y;
-#pragma unroll
-            for (int i = 0; i < V; ++i) y.v[i] = from_f32<T>(fmaf((to_f32(x[u].v[i]) - mean) * rstd, g[i], b[i]));
-            store_vec<T, V>(out + c, y);
+            if (a.gamma) load_weight<T, V>(a.gamma, a.weight_f32, c, gv);
+            if (a.beta) load_weight<T, V>(a.beta, a.weight_f32, c, bv);
         }
+    };
+    if constexpr (F::hold) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) weights(g[u], b[u], (u * G + t) * V);
+    }
+    int flip = 0;  // the sums of consecutive rows use other places: one barrier a sum is enough
+    for (int64_t r0 = row0; r0 < a.rows; r0 += step) {
+        Vec<T, V>(&x)[U] = ring[0];
+        const int64_t row = r0 + sub;
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[V];
+            x[u].unpack(f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[0] += f[i];
+        }
+        row_sums<G>(sum, s_sum[2 * flip]);
+        const float mean = sum[0] * a.inv_cols;
+        float sq[1] = {0.f};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if ((u * G + t) * V < a.cols) {
+                float f[V];
+                x[u].unpack(f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sq[0] = fmaf(f[i] - mean, f[i] - mean, sq[0]);
+            }
+        }
+        row_sums<G>(sq, s_sum[2 * flip + 1]);
+        flip ^= 1;
+        const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sq[0], a.inv_cols, a.eps)));
+        if (row < a.rows) {
+            if (t == 0 && a.mean) {
+                a.mean[row] = mean;
+                a.rstd[row] = rstd;
+            }
+            T* out = static_cast<T*>(a.out) + row * a.out_stride;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = (u * G + t) * V;
+                if constexpr (!F::hold) weights(g[0], b[0], c);
+                if (c < a.cols) {
+                    float f[V];
+                    x[u].unpack(f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        f[i] = fmaf((f[i] - mean) * rstd, g[F::hold ? u : 0][i], b[F::hold ? u : 0][i]);
+                    Vec<T, V> y;
+                    y.pack(f);
+                    store_vec<T, V>(out + c, y);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < F::ahead; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) ring[k][u] = ring[k + 1][u];
+        load(ring[F::ahead], row + (F::ahead + 1) * step);
     }
 }
 
 template <class T, int V, int G, int U>
 int launch(const NormArgs& a, cudaStream_t s) {
-    const int64_t blocks = (a.rows + RowShape<G>::rows - 1) / RowShape<G>::rows;
-    if (blocks > INT32_MAX) return IX_ERR_UNSUPPORTED;
-    norm_fwd_kernel<T, V, G, U><<<static_cast<unsigned>(blocks), RowShape<G>::threads, 0, s>>>(a);
+    using F = Fwd<T, V, G, U>;
+    const int64_t want = (a.rows + F::rows - 1) / F::rows, most = kSms * F::ctas;
+    norm_fwd_kernel<T, V, G, U><<<static_cast<int>(want < most ? want : most), F::threads, 0, s>>>(a);
     return launch_status();
 }
 
@@ -98,11 +134,11 @@ int dispatch(const NormArgs& a, cudaStream_t s) {
         if (n <= 16) return launch<T, W, 16, 1>(a, s);
         if (n <= 32) return launch<T, W, 32, 1>(a, s);
         if (n <= 64) return launch<T, W, 32, 2>(a, s);
-        if (n <= 128) return launch<T, W, 32, 4>(a, s);
+        if (n <= 128) return launch<T, W, 64, 2>(a, s);
         if (n <= 256) return launch<T, W, 128, 2>(a, s);
         if (n <= 512) return launch<T, W, 256, 2>(a, s);
-        if (n <= 1024) return launch<T, W, 256, 4>(a, s);
-        if (n <= 2048) return launch<T, W, 512, 4>(a, s);
+        if (n <= 1024) return launch<T, W, 512, 2>(a, s);
+        if (n <= 2048) return launch<T, W, 1024, 2>(a, s);
         if (n <= 4096) return launch<T, W, 1024, 4>(a, s);
         if constexpr (W == 4) return launch<T, W, 1024, 8>(a, s);
         return IX_ERR_UNSUPPORTED;
@@ -110,15 +146,14 @@ int dispatch(const NormArgs& a, cudaStream_t s) {
     const int n = a.cols;
     if (n <= 32) return launch<T, 1, 32, 1>(a, s);
     if (n <= 128) return launch<T, 1, 32, 4>(a, s);
-    if (n <= 512) return launch<T, 1, 32, 16>(a, s);
-    if (n <= 2048) return launch<T, 1, 128, 16>(a, s);
+    if (n <= 512) return launch<T, 1, 64, 8>(a, s);
+    if (n <= 2048) return launch<T, 1, 256, 8>(a, s);
     if (n <= 8192) return launch<T, 1, 512, 16>(a, s);
     return launch<T, 1, 1024, 32>(a, s);
 }
 
 }  // namespace
 }  // namespace dsix
-
 using namespace dsix;
 
 extern "C" int ix_layer_norm(const void* x, int64_t x_stride, const void* gamma, const void* beta, int weight_dtype,

@@ -225,7 +225,8 @@ __device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, 
     }
     // the new blocks' table entries: no row above reads them
     const int32_t taken = a.batch ? cb[a.batch] : 0;
-    for (int64_t k = tid; k < taken; k += threads) {
+    // (the last threads first: in a small step they have no rows)
+    for (int64_t k = threads - 1 - tid; k < taken; k += threads) {
         const int b = find_request(cb, a.batch, static_cast<int32_t>(k));
         const int64_t j = static_cast<int64_t>(blocks_of(a, max(__ldg(a.cached + b), 0))) + (k - cb[b]);
         if (j < a.width)
@@ -290,7 +291,7 @@ extern "C" int ix_plan_step(const int32_t* cached_lens, const int32_t* new_lens,
                      bt_stride, bt_width, context_lens, cu_new, cu_ctx, cu_blocks, slot_mapping, positions,
                      row_req, row_len, ks, ke, rows, st};
     const int64_t want = (rows + kThreads * kRows - 1) / (kThreads * kRows);
-    const int grid = static_cast<int>(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
+    const int grid = static_cast<int>(want < 1 ? 1 : want > 4 * sms ? 4 * sms : want);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (batch <= kFusedBatch) {
         const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);

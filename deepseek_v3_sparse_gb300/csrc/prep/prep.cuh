@@ -11,33 +11,73 @@
 
 namespace dsix {
 
-template <class T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+__device__ __forceinline__ void from_f32(float f, __nv_bfloat16& v) { v = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void from_f32(float f, __half& v) { v = __float2half_rn(f); }
+__device__ __forceinline__ void from_f32(float f, float& v) { v = f; }
+
+__device__ __forceinline__ float2 to_f32(__nv_bfloat162 v) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
+    return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float2 to_f32(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ void from_f32(float a, float b, __nv_bfloat162& v) { v = __floats2bfloat162_rn(a, b); }
+__device__ __forceinline__ void from_f32(float a, float b, __half2& v) { v = __floats2half2_rn(a, b); }
 
 template <class T>
-__device__ __forceinline__ T from_f32(float v);
+struct Pair;  // two elements in one register
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+struct Pair<__nv_bfloat16> { using type = __nv_bfloat162; };
 template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+struct Pair<__half> { using type = __half2; };
 
-// V elements that are loaded and stored as one access (V * sizeof(T) <= 16 bytes)
+// V elements that are loaded and stored as one access (V * sizeof(T) <= 16
+// bytes); two 16-bit elements lie in one register and are converted together.
 template <class T, int V>
 struct alignas(V * sizeof(T)) Vec {
+    static constexpr bool paired = sizeof(T) == 2 && V % 2 == 0;
     T v[V];
+
+    __device__ __forceinline__ void unpack(float (&f)[V]) const {
+        if constexpr (paired) {
+            using P = typename Pair<T>::type;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 q = to_f32(reinterpret_cast<const P*>(v)[i]);
+                f[2 * i] = q.x;
+                f[2 * i + 1] = q.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = to_f32(v[i]);
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[V]) {
+        if constexpr (paired) {
+            using P = typename Pair<T>::type;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) from_f32(f[2 * i], f[2 * i + 1], reinterpret_cast<P*>(v)[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) from_f32(f[i], v[i]);
+        }
+    }
 };
 
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
     return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> zero_vec() {
+    Vec<T, V> z;
+    const float f[V] = {};
+    z.pack(f);
+    return z;
 }
 
 template <class T, int V>
@@ -62,6 +102,20 @@ __device__ __forceinline__ void load_f32(const float* p, float (&f)[V]) {
         for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
     }
 }
+
+// Division of n < 2^31 by a number known at launch: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (high word of n m + n) >> s
+// (T. Granlund and P. Montgomery, "Division by invariant integers using
+// multiplication", 1994).
+struct FastDiv {
+    uint32_t d = 1, m = 1, s = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by) {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
 
 inline bool aligned_to(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;

@@ -8,39 +8,94 @@ namespace {
 constexpr int kMaxPairs = 128;
 constexpr int kThreads = 256;
 constexpr int kMaxHeads = 65536, kMaxDim = 65536;
+constexpr int64_t kMaxItems = 1ll << 30;
 
 // ---------------------------------------------------------------------------
 // ix_rope_table.  The angle p * f of pair f at position p is held in turns, as
-// a 64-bit fixed-point fraction: with F = round(f / (2 pi) * 2^64) mod 2^64, the
-// wrapping product p * F is the angle modulo one turn, exact but for F's one
-// rounding (p * 2^-65 turns).  The nearest quarter turn is split off in
-// integers; what is left, at most an eighth of a turn, goes through sincospif in
-// f32 with its relative accuracy intact, also next to the zeros.
+// a 64-bit fixed-point fraction: with F = f / (2 pi) * 2^64 mod 2^64, rounded,
+// the wrapping product p * F is the angle modulo one turn, exact but for F's
+// rounding.  The nearest quarter turn is split off in integers; what is left, an
+// eighth of a turn at most, goes to radians in f32 with its relative accuracy
+// intact, also next to the zeros, and through the Taylor series of sine and
+// cosine: at pi / 4 the first terms left out are x^11 / 11! = 1.8e-9 and
+// x^12 / 12! = 1.2e-10, below a tenth of a rounding.
+//
+// A thread keeps W pairs and walks down the positions with one 64-bit addition
+// a pair; W = 4 makes its stores 16 bytes wide.
 // ---------------------------------------------------------------------------
 struct TurnTable {
     uint64_t step[kMaxPairs];
 };
 
+__device__ __forceinline__ void sincos_turn(uint64_t turn, float amplitude, float& s, float& c) {
+    const uint64_t quarter = (turn + (1ull << 61)) >> 62;
+    const int64_t rest = static_cast<int64_t>(turn - (quarter << 62));
+    const float x = __ll2float_rn(rest) * static_cast<float>(6.283185307179586 * 0x1p-64);
+    const float q = x * x;
+    float ps = fmaf(q, 1.f / 362880, -1.f / 5040);
+    ps = fmaf(q, ps, 1.f / 120);
+    ps = fmaf(q, ps, -1.f / 6);
+    const float sn = fmaf(x * q, ps, x);
+    float pc = fmaf(q, -1.f / 3628800, 1.f / 40320);
+    pc = fmaf(q, pc, -1.f / 720);
+    pc = fmaf(q, pc, 1.f / 24);
+    pc = fmaf(q, pc, -0.5f);
+    const float cs = fmaf(q, pc, 1.f);
+    const uint32_t k = static_cast<uint32_t>(quarter);
+    s = amplitude * (k & 1 ? cs : sn);
+    c = amplitude * (k & 1 ? sn : cs);
+    if (k & 2) s = -s;
+    if ((k + 1) & 2) c = -c;
+}
+
+template <int W>
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TurnTable f, int pairs,
                                                               int64_t first, int64_t n, float amplitude,
                                                               float* __restrict__ out) {
-    const int64_t total = n * pairs;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = i / pairs;
-        const int p = static_cast<int>(i - r * pairs);
-        const uint64_t turn = static_cast<uint64_t>(first + r) * f.step[p];
-        const uint64_t quarter = (turn + (1ull << 61)) >> 62;
-        const int64_t rest = static_cast<int64_t>(turn - (quarter << 62));
-        float s, c;
-        sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
-        const bool swap = quarter & 1;
-        float cs = swap ? s : c, sn = swap ? c : s;
-        if (quarter == 1 || quarter == 2) cs = -cs;
-        if (quarter == 2 || quarter == 3) sn = -sn;
-        out[r * 2 * pairs + p] = cs * amplitude;
-        out[r * 2 * pairs + pairs + p] = sn * amplitude;
+    const int across = pairs / W, down = kThreads / across;  // threads along a row, rows of a CTA at a time
+    const int q = threadIdx.x % across, sub = threadIdx.x / across;
+    if (sub >= down) return;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * down;
+    int64_t r = static_cast<int64_t>(blockIdx.x) * down + sub;
+    uint64_t turn[W], step[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const uint64_t one = f.step[q * W + i];
+        turn[i] = static_cast<uint64_t>(first + r) * one;
+        step[i] = static_cast<uint64_t>(stride) * one;
     }
+    for (; r < n; r += stride) {
+        Vec<float, W> s, c;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            sincos_turn(turn[i], amplitude, s.v[i], c.v[i]);
+            turn[i] += step[i];
+        }
+        float* row = out + r * 2 * pairs + q * W;
+        store_vec<float, W>(row, c);
+        store_vec<float, W>(row + pairs, s);
+    }
+}
+
+// f / (2 pi) * 2^64 mod 2^64, from the 128 leading bits of 1 / (2 pi): the
+// product with f's 53 bits is exact, and |f| < 2^20 leaves an error far below
+// the final rounding.  Integers only: the same on every host.
+uint64_t turns_of(double f) {
+    int e = 0;
+    const double m = frexp(fabs(f), &e);  // [0.5, 1)
+    const uint64_t mant = static_cast<uint64_t>(ldexp(m, 53));  // |f| = mant * 2^(e - 53)
+    const uint64_t hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;  // 1 / (2 pi) * 2^128
+    const unsigned __int128 p0 = static_cast<unsigned __int128>(mant) * lo;
+    const unsigned __int128 p1 = static_cast<unsigned __int128>(mant) * hi + static_cast<uint64_t>(p0 >> 64);
+    // the product is p1 * 2^64 + (low word of p0), in units of 2^(e - 53 - 128);
+    // in units of 2^-64 it is shifted right by 117 - e = 64 + (53 - e)
+    const int shift = 53 - e;  // of p1; e <= 20 keeps it above 32
+    uint64_t turns = 0;
+    if (shift <= 120) {
+        const unsigned __int128 rounded = p1 + (static_cast<unsigned __int128>(1) << (shift - 1));
+        turns = static_cast<uint64_t>(rounded >> shift);
+    }
+    return f < 0 ? 0 - turns : turns;
 }
 
 // ---------------------------------------------------------------------------
@@ -48,22 +103,25 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
 // holds V whole pairs (half layout: a vector of each half; interleaved: two
 // adjacent vectors), a copy item two vectors of the rest.  A thread has one item
 // of kHeads heads of a token, so the cosines and sines it read serve all of
-// them.
+// them, and 2 * kHeads loads are in flight.  A token's pair items come before
+// its copy items: whole warps turn or copy, and neighbouring lanes have
+// neighbouring vectors.
 // ---------------------------------------------------------------------------
 struct RopeSide {
     const void* x;
     void* out;
     int heads, groups;  // groups = ceil(heads / kHeads): head u of group g is g + u * groups
     int64_t xt, xh, ot, oh;
+    uint32_t turn_items;  // groups * pair_items: a token's first items
+    FastDiv per_token;    // items of a token
 };
 
 struct RopeArgs {
     RopeSide side[2];
-    int64_t blocks0;  // CTAs of side 0
+    uint32_t blocks0;  // CTAs of side 0
     int64_t tokens;
-    int pair_items, items;  // per head
-    int dim, offset, rot, copy_vecs;
-    int interleaved;
+    FastDiv pair_items, copy_items;  // per head
+    int offset, rot, copy_vecs;
     float sign;
     const int64_t* positions;
     const float* cos_sin;
@@ -71,27 +129,30 @@ struct RopeArgs {
     int* status;
 };
 
-template <class T, int V, int kHeads>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-    const int which = blockIdx.x >= a.blocks0;
+template <class T, int V, int kHeads, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    const bool which = blockIdx.x >= a.blocks0;
     const RopeSide& d = a.side[which];
-    const int64_t idx = (static_cast<int64_t>(blockIdx.x) - (which ? a.blocks0 : 0)) * kThreads + threadIdx.x;
-    const int64_t per_token = static_cast<int64_t>(d.groups) * a.items;
-    const int64_t t = idx / per_token;
+    const uint32_t idx = (blockIdx.x - (which ? a.blocks0 : 0)) * kThreads + threadIdx.x;
+    const uint32_t t = d.per_token.of(idx);
     if (t >= a.tokens) return;
-    const int rest = static_cast<int>(idx - t * per_token);
-    const int g = rest / a.items, item = rest - g * a.items;
+    uint32_t rest = idx - t * d.per_token.d;
+    const bool first = rest == 0;
+    const bool pair = rest < d.turn_items;
+    if (!pair) rest -= d.turn_items;
+    const FastDiv& items = pair ? a.pair_items : a.copy_items;
+    const int g = static_cast<int>(items.of(rest)), item = static_cast<int>(rest - g * items.d);
     const int64_t p = __ldg(a.positions + t);
-    const T* x = static_cast<const T*>(d.x) + t * d.xt;
-    T* out = static_cast<T*>(d.out) + t * d.ot;
-    const bool pair = item < a.pair_items;
+    const T* x = static_cast<const T*>(d.x) + t * d.xt + g * d.xh;
+    T* out = static_cast<T*>(d.out) + t * d.ot + g * d.oh;
+    const int64_t xs = d.groups * d.xh, os = d.groups * d.oh;  // from a head of this thread to its next
     int e0, e1;  // first elements of the item's two vectors
     bool has1 = true;
     if (pair) {
-        e0 = a.offset + (a.interleaved ? 2 : 1) * item * V;
-        e1 = a.interleaved ? e0 + V : e0 + a.rot / 2;
+        e0 = a.offset + (kInterleaved ? 2 : 1) * item * V;
+        e1 = kInterleaved ? e0 + V : e0 + a.rot / 2;
     } else {
-        const int v = 2 * (item - a.pair_items);
+        const int v = 2 * item;
         e0 = v * V < a.offset ? v * V : v * V + a.rot;
         e1 = (v + 1) * V < a.offset ? (v + 1) * V : (v + 1) * V + a.rot;
         has1 = v + 1 < a.copy_vecs;
@@ -99,14 +160,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     Vec<T, V> v0[kHeads], v1[kHeads];
 #pragma unroll
     for (int u = 0; u < kHeads; ++u) {
-        const int h = g + u * d.groups;
-        if (h < d.heads) {
-            v0[u] = load_vec<T, V>(x + h * d.xh + e0);
-            if (has1) v1[u] = load_vec<T, V>(x + h * d.xh + e1);
+        if (g + u * d.groups < d.heads) {
+            v0[u] = load_vec<T, V>(x + u * xs + e0);
+            if (has1) v1[u] = load_vec<T, V>(x + u * xs + e1);
         }
     }
     if (p < 0 || p >= a.max_pos) {
-        if (rest == 0) flag(a.status, IX_DEV_BAD_POSITION);
+        if (first) flag(a.status, IX_DEV_BAD_POSITION);
         return;
     }
     if (pair) {
@@ -118,71 +178,93 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         for (int i = 0; i < V; ++i) s[i] *= a.sign;
 #pragma unroll
         for (int u = 0; u < kHeads; ++u) {
-            if (g + u * d.groups >= d.heads) break;
-            float e[2 * V];
+            float y[V], z[V];
+            v0[u].unpack(y);
+            v1[u].unpack(z);
+            // the roundings are spelled out: every variant gives the same bits
+            auto turn = [&](int i, float& m, float& n) {
+                const float k = m;
+                m = fmaf(-n, s[i], __fmul_rn(k, c[i]));
+                n = fmaf(k, s[i], __fmul_rn(n, c[i]));
+            };
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                e[i] = to_f32(v0[u].v[i]);
-                e[V + i] = to_f32(v1[u].v[i]);
+                if constexpr (kInterleaved && V > 1)
+                    turn(i, i < V / 2 ? y[2 * i] : z[2 * i - V], i < V / 2 ? y[2 * i + 1] : z[2 * i + 1 - V]);
+                else
+                    turn(i, y[i], z[i]);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int ia = a.interleaved ? 2 * i : i, ib = a.interleaved ? 2 * i + 1 : V + i;
-                const float y = e[ia], z = e[ib];
-                // the roundings are spelled out: every variant gives the same bits
-                e[ia] = fmaf(-z, s[i], __fmul_rn(y, c[i]));
-                e[ib] = fmaf(y, s[i], __fmul_rn(z, c[i]));
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v0[u].v[i] = from_f32<T>(e[i]);
-                v1[u].v[i] = from_f32<T>(e[V + i]);
-            }
+            v0[u].pack(y);
+            v1[u].pack(z);
         }
     }
 #pragma unroll
     for (int u = 0; u < kHeads; ++u) {
-        const int h = g + u * d.groups;
-        if (h < d.heads) {
-            store_vec<T, V>(out + h * d.oh + e0, v0[u]);
-            if (has1) store_vec<T, V>(out + h * d.oh + e1, v1[u]);
+        if (g + u * d.groups < d.heads) {
+            store_vec<T, V>(out + u * os + e0, v0[u]);
+            if (has1) store_vec<T, V>(out + u * os + e1, v1[u]);
         }
     }
 }
 
 template <class T, int V, int kHeads>
-int launch(RopeArgs& a, bool copies, cudaStream_t s) {
-    a.pair_items = a.rot / (2 * V);
-    a.copy_vecs = copies ? (a.dim - a.rot) / V : 0;
-    a.items = a.pair_items + (a.copy_vecs + 1) / 2;
-    int64_t blocks[2] = {0, 0};
-    for (int w = 0; w < 2; ++w) {
-        RopeSide& d = a.side[w];
+int launch(RopeArgs& a, int dim, bool copies, bool interleaved, cudaStream_t s) {
+    const int pair_items = a.rot / (2 * V);
+    a.copy_vecs = copies ? (dim - a.rot) / V : 0;
+    const int copy_items = (a.copy_vecs + 1) / 2;
+    a.pair_items = FastDiv(pair_items);
+    a.copy_items = FastDiv(copy_items ? copy_items : 1);
+    int64_t per_token = 0;
+    for (RopeSide& d : a.side) {
         if (!d.x) continue;
         d.groups = (d.heads + kHeads - 1) / kHeads;
-        blocks[w] = (a.tokens * d.groups * a.items + kThreads - 1) / kThreads;
+        d.turn_items = static_cast<uint32_t>(d.groups) * pair_items;
+        const int64_t items = static_cast<int64_t>(d.groups) * (pair_items + copy_items);
+        if (items > kMaxItems) return IX_ERR_UNSUPPORTED;
+        d.per_token = FastDiv(static_cast<uint32_t>(items));
+        per_token = items > per_token ? items : per_token;
     }
-    a.blocks0 = blocks[0];
-    if (blocks[0] + blocks[1] > INT32_MAX) return IX_ERR_UNSUPPORTED;
-    rope_kernel<T, V, kHeads><<<static_cast<unsigned>(blocks[0] + blocks[1]), kThreads, 0, s>>>(a);
-    return launch_status();
+    // indexes are formed in 31 bits: very long calls go out in runs of tokens
+    const int64_t run = kMaxItems / per_token, tokens = a.tokens;
+    const RopeSide side[2] = {a.side[0], a.side[1]};
+    const int64_t* positions = a.positions;
+    for (int64_t t0 = 0; t0 < tokens; t0 += run) {
+        a.tokens = tokens - t0 < run ? tokens - t0 : run;
+        a.positions = positions + t0;
+        uint32_t blocks[2] = {0, 0};
+        for (int w = 0; w < 2; ++w) {
+            if (!side[w].x) continue;
+            a.side[w].x = static_cast<const T*>(side[w].x) + t0 * side[w].xt;
+            a.side[w].out = static_cast<T*>(side[w].out) + t0 * side[w].ot;
+            blocks[w] = static_cast<uint32_t>((a.tokens * side[w].per_token.d + kThreads - 1) / kThreads);
+        }
+        a.blocks0 = blocks[0];
+        if (interleaved)
+            rope_kernel<T, V, kHeads, true><<<blocks[0] + blocks[1], kThreads, 0, s>>>(a);
+        else
+            rope_kernel<T, V, kHeads, false><<<blocks[0] + blocks[1], kThreads, 0, s>>>(a);
+        const int rc = launch_status();
+        if (rc != IX_OK) return rc;
+    }
+    return IX_OK;
 }
 
 template <class T>
-int dispatch(RopeArgs& a, bool copies, int sms, cudaStream_t s) {
+int dispatch(RopeArgs& a, int dim, bool copies, bool interleaved, int sms, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     // 16-byte vectors where every pointer, stride and part of the head allows them
     bool wide = a.offset % W == 0 && (a.rot / 2) % W == 0 && aligned16(a.cos_sin) &&
-                (!copies || (a.dim - a.offset - a.rot) % W == 0);
+                (!copies || (dim - a.offset - a.rot) % W == 0);
     for (const RopeSide& d : a.side)
         if (d.x)
             wide = wide && aligned16(d.x) && aligned16(d.out) && d.xt % W == 0 && d.ot % W == 0 &&
                    (d.heads == 1 || (d.xh % W == 0 && d.oh % W == 0));
-    const int64_t values = a.tokens * a.side[0].heads * a.dim;
+    const int64_t values = a.tokens * a.side[0].heads * dim;
     // four heads a thread once that leaves every SM its share of threads
     const bool many = values * static_cast<int64_t>(sizeof(T)) >= static_cast<int64_t>(sms) * 2048 * 128;
-    if (wide) return many ? launch<T, W, 4>(a, copies, s) : launch<T, W, 1>(a, copies, s);
-    return many ? launch<T, 1, 4>(a, copies, s) : launch<T, 1, 1>(a, copies, s);
+    if (wide)
+        return many ? launch<T, W, 4>(a, dim, copies, interleaved, s) : launch<T, W, 1>(a, dim, copies, interleaved, s);
+    return many ? launch<T, 1, 4>(a, dim, copies, interleaved, s) : launch<T, 1, 1>(a, dim, copies, interleaved, s);
 }
 
 // an output whose elements are all distinct: heads within tokens, or tokens within heads
@@ -234,21 +316,22 @@ extern "C" int ix_rope_table(const double* inv_freq, int rot, int64_t first, int
     if (!inv_freq) return IX_ERR_NULL;
     TurnTable f{};
     for (int i = 0; i < rot / 2; ++i) {
-        if (!isfinite(inv_freq[i])) return IX_ERR_UNSUPPORTED;
-        long double turns = static_cast<long double>(inv_freq[i]) / 6.283185307179586476925286766559L;
-        turns -= floorl(turns);  // [0, 1]: whole turns per position change nothing
-        const long double scaled = roundl(turns * 0x1p64L);
-        f.step[i] = scaled >= 0x1p64L ? 0 : static_cast<uint64_t>(scaled);
+        if (!(fabs(inv_freq[i]) < 0x1p20)) return IX_ERR_UNSUPPORTED;
+        f.step[i] = turns_of(inv_freq[i]);
     }
     if (n == 0) return IX_OK;
     if (!cos_sin) return IX_ERR_NULL;
     if (!aligned16(cos_sin)) return IX_ERR_ALIGN;
     const int sms = num_sms();
     if (sms <= 0) return IX_ERR_CUDA;
-    const int64_t want = (n * (rot / 2) + kThreads - 1) / kThreads, cap = static_cast<int64_t>(sms) * 8;
-    rope_table_kernel<<<static_cast<int>(want < cap ? want : cap), kThreads, 0,
-                        reinterpret_cast<cudaStream_t>(stream)>>>(f, rot / 2, first, n,
-                                                                  static_cast<float>(amplitude), cos_sin);
+    const int pairs = rot / 2, per_cta = kThreads / (pairs % 4 ? pairs : pairs / 4);  // positions
+    const int64_t want = (n + per_cta - 1) / per_cta, cap = static_cast<int64_t>(sms) * 8;
+    const int grid = static_cast<int>(want < cap ? want : cap);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (pairs % 4)
+        rope_table_kernel<1><<<grid, kThreads, 0, s>>>(f, pairs, first, n, static_cast<float>(amplitude), cos_sin);
+    else
+        rope_table_kernel<4><<<grid, kThreads, 0, s>>>(f, pairs, first, n, static_cast<float>(amplitude), cos_sin);
     return launch_status();
 }
 
@@ -285,13 +368,11 @@ extern "C" int ix_rope(const ix_rope_tensor* x, const ix_rope_tensor* x2, int dt
             copies = copies || head_dim > rot;
         }
         a.side[w] = {d->x, d->out, d->heads, 0, d->x_token_stride, d->x_head_stride, d->out_token_stride,
-                     d->out_head_stride};
+                     d->out_head_stride, 0, FastDiv()};
     }
     a.tokens = tokens;
-    a.dim = head_dim;
     a.offset = offset;
     a.rot = rot;
-    a.interleaved = (flags & IX_ROPE_INTERLEAVED) ? 1 : 0;
     a.sign = (flags & IX_ROPE_INVERSE) ? -1.f : 1.f;
     a.positions = positions;
     a.cos_sin = cos_sin;
@@ -300,7 +381,8 @@ extern "C" int ix_rope(const ix_rope_tensor* x, const ix_rope_tensor* x2, int dt
     const int sms = num_sms();
     if (!a.status || sms <= 0) return IX_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == IX_BF16) return dispatch<__nv_bfloat16>(a, copies, sms, s);
-    if (dtype == IX_FP16) return dispatch<__half>(a, copies, sms, s);
-    return dispatch<float>(a, copies, sms, s);
+    const bool inter = flags & IX_ROPE_INTERLEAVED;
+    if (dtype == IX_BF16) return dispatch<__nv_bfloat16>(a, head_dim, copies, inter, sms, s);
+    if (dtype == IX_FP16) return dispatch<__half>(a, head_dim, copies, inter, sms, s);
+    return dispatch<float>(a, head_dim, copies, inter, sms, s);
 }

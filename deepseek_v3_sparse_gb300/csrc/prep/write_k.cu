@@ -1,10 +1,12 @@
 // write_k.cu -- ix_norm_rope_write_k: layer norm, rotary positions, fp8 coding
 // and the paged write of the indexer key, one pass over the token.
 //
-// Eight lanes hold a token, 16 consecutive values each, so the three reductions
-// of a token (mean, centred squares, amax) are three shuffles each, and a
-// rotated pair lies in one lane (interleaved; rot = 16) or in two lanes
-// rot / 32 apart, each of which forms its own half of the pair.
+// Eight lanes hold a token, two vectors of eight values each, cut as ix_rope
+// cuts a head: rot / 16 lanes have eight whole pairs (half layout: a vector of
+// each half; interleaved: two adjacent vectors), the others two vectors of the
+// rest.  So no pair crosses a lane, and the three reductions of a token (mean,
+// centred squares, amax) are three shuffles each.  The next token's loads are in
+// flight behind the present one's arithmetic.
 #include <float.h>
 
 #include "prep.cuh"
@@ -27,7 +29,7 @@ struct WriteArgs {
     const int64_t* positions;
     const float* cos_sin;
     int64_t max_pos;
-    int rot, offset, interleaved;
+    int rot, offset;
     const int64_t* slots;
     uint8_t* cache;
     int64_t num_blocks;
@@ -41,66 +43,95 @@ __device__ __forceinline__ float sum8(float v) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const WriteArgs a) {
-    constexpr int V = 16 / sizeof(T), NV = kPer / V;
-    const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
-    const T* kin = static_cast<const T*>(a.k);
-    float g[kPer], bt[kPer];
-    load_f32<kPer>(a.gamma + sub * kPer, g);
-    load_f32<kPer>(a.beta + sub * kPer, bt);
-    // where this lane's values lie in the rotated part
-    const int e0 = sub * kPer - a.offset;  // a multiple of 16
-    const bool rotated = e0 >= 0 && e0 < a.rot;
-    const int half = a.rot >> 1;
-    const bool second = e0 >= half;
-    const int apart = a.rot >= 32 ? a.rot / 32 : 0;
-    const int other = (lane & ~(kLanes - 1)) | ((sub + (second ? -apart : apart)) & (kLanes - 1));
-    const int64_t tokens = (static_cast<int64_t>(gridDim.x) * kThreads) / kLanes;
-    // the loop runs for the warp's first token, so that all lanes meet in the shuffles
-    for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes; t0 - (lane / kLanes) < a.n;
-         t0 += tokens) {
-        const bool live = t0 < a.n;
-        float x[kPer];
-        int64_t slot = -1, pos = 0;
+struct Token {
+    static constexpr int V = 16 / sizeof(T), N = 8 / V;
+    Vec<T, V> lo[N], hi[N];  // values e0 .. e0 + 7 and e1 .. e1 + 7
+    int64_t slot, pos;
+
+    __device__ __forceinline__ void load(const WriteArgs& a, int64_t t, int e0, int e1) {
+        const bool live = t < a.n;
+        const T* row = static_cast<const T*>(a.k) + t * a.k_stride;
+        slot = live ? __ldg(a.slots + t) : -1;
+        pos = live ? __ldg(a.positions + t) : 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = 0.f;
-        if (live) {
-            slot = __ldg(a.slots + t0);
-            pos = __ldg(a.positions + t0);
-            const T* row = kin + t0 * a.k_stride + sub * kPer;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const Vec<T, V> v = load_vec<T, V>(row + j * V);
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[j * V + i] = to_f32(v.v[i]);
-            }
+        for (int i = 0; i < N; ++i) {
+            lo[i] = live ? load_vec<T, V>(row + e0 + i * V) : zero_vec<T, V>();
+            hi[i] = live ? load_vec<T, V>(row + e1 + i * V) : zero_vec<T, V>();
         }
+    }
+    __device__ __forceinline__ void unpack(float (&x)[kPer]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float f[V];
+            lo[i].unpack(f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[i * V + j] = f[j];
+            hi[i].unpack(f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[8 + i * V + j] = f[j];
+        }
+    }
+};
+
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = cvt_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+template <class T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_write_kernel(const WriteArgs a) {
+    const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
+    const int pair_lanes = a.rot / 16;
+    const bool rotated = sub < pair_lanes;
+    int e0, e1;
+    if (rotated) {
+        e0 = a.offset + (kInterleaved ? 16 : 8) * sub;
+        e1 = kInterleaved ? e0 + 8 : e0 + a.rot / 2;
+    } else {
+        const int v = 16 * (sub - pair_lanes);
+        e0 = v < a.offset ? v : v + a.rot;
+        e1 = v + 8 < a.offset ? v + 8 : v + 8 + a.rot;
+    }
+    const int64_t tokens = (static_cast<int64_t>(gridDim.x) * kThreads) / kLanes;
+    int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
+    Token<T> next;
+    next.load(a, t, e0, e1);
+    float g[kPer], b[kPer];
+    {
+        float f[8];
+        load_f32<8>(a.gamma + e0, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = f[i];
+        load_f32<8>(a.gamma + e1, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[8 + i] = f[i];
+        load_f32<8>(a.beta + e0, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = f[i];
+        load_f32<8>(a.beta + e1, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[8 + i] = f[i];
+    }
+    // the loop runs for the warp's first token, so that all lanes meet in the shuffles
+    for (; t - (lane / kLanes) < a.n; t += tokens) {
+        float x[kPer];
+        next.unpack(x);
+        const int64_t slot = next.slot, pos = next.pos;
         const int64_t blk = slot / kBlock;
         bool write = slot >= 0;
         if (write && (blk >= a.num_blocks || pos < 0 || pos >= a.max_pos)) {
             if (sub == 0) flag(a.status, blk >= a.num_blocks ? IX_DEV_BAD_SLOT : IX_DEV_BAD_POSITION);
             write = false;
         }
-        float c[kPer], s[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) c[i] = s[i] = 0.f;
+        float c[8], s[8];
         if (write && rotated) {
-            const float* row = a.cos_sin + pos * a.rot;
-            if (a.interleaved || a.rot == 16) {  // eight pairs in this lane
-                const int p0 = a.interleaved ? e0 >> 1 : 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 cq = __ldg(reinterpret_cast<const float4*>(row + p0) + i);
-                    const float4 sq = __ldg(reinterpret_cast<const float4*>(row + half + p0) + i);
-                    c[4 * i] = cq.x; c[4 * i + 1] = cq.y; c[4 * i + 2] = cq.z; c[4 * i + 3] = cq.w;
-                    s[4 * i] = sq.x; s[4 * i + 1] = sq.y; s[4 * i + 2] = sq.z; s[4 * i + 3] = sq.w;
-                }
-            } else {
-                const int p0 = second ? e0 - half : e0;
-                load_f32<kPer>(row + p0, c);
-                load_f32<kPer>(row + half + p0, s);
-            }
+            const float* row = a.cos_sin + pos * a.rot + 8 * sub;
+            load_f32<8>(row, c);
+            load_f32<8>(row + a.rot / 2, s);
         }
+        next.load(a, t + tokens, e0, e1);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) sum += x[i];
@@ -113,31 +144,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const WriteAr
         }
         const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sum8(sq), 1.f / kDim, a.eps)));
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = fmaf(x[i] * rstd, g[i], bt[i]);
-        if (a.interleaved) {
-            if (rotated) {
+        for (int i = 0; i < kPer; ++i) x[i] = fmaf(x[i] * rstd, g[i], b[i]);
+        if (write && rotated) {
 #pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) {
-                    const float p = x[2 * i], q = x[2 * i + 1];
-                    x[2 * i] = p * c[i] - q * s[i];
-                    x[2 * i + 1] = p * s[i] + q * c[i];
-                }
-            }
-        } else if (a.rot == 16) {
-            if (rotated) {
-#pragma unroll
-                for (int i = 0; i < kPer / 2; ++i) {
-                    const float p = x[i], q = x[i + kPer / 2];
-                    x[i] = p * c[i] - q * s[i];
-                    x[i + kPer / 2] = p * s[i] + q * c[i];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float y = __shfl_sync(0xffffffffu, x[i], other);
-                // the first of a pair: a c - b s; the second: a s + b c
-                if (rotated) x[i] = second ? fmaf(y, s[i], x[i] * c[i]) : fmaf(-y, s[i], x[i] * c[i]);
+            for (int i = 0; i < 8; ++i) {
+                float& p = x[kInterleaved ? 2 * i : i];
+                float& q = x[kInterleaved ? 2 * i + 1 : 8 + i];
+                const float y = p;
+                p = fmaf(-q, s[i], y * c[i]);
+                q = fmaf(y, s[i], q * c[i]);
             }
         }
         float amax = 0.f;
@@ -147,17 +162,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const WriteAr
         for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float scale = fmaxf(__fdiv_rn(amax, 448.f), FLT_MIN);
         if (write) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = cvt_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
-                       (cvt_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16);
+            // z comes with roundings of its own, so its quotient by the scale is
+            // formed with one more, as a product with the reciprocal
+            const float inv = __frcp_rn(scale);
             const int at = static_cast<int>(slot % kBlock);
             uint8_t* base = a.cache + blk * kBlockBytes;
-            *reinterpret_cast<uint4*>(base + at * kDim + sub * kPer) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint2*>(base + at * kDim + e0) = codes8(x, inv);
+            *reinterpret_cast<uint2*>(base + at * kDim + e1) = codes8(x + 8, inv);
             if (sub == 0) *reinterpret_cast<float*>(base + kBlock * kDim + 4 * at) = scale;
         }
     }
+}
+
+template <class T>
+void launch(const WriteArgs& a, bool interleaved, int grid, cudaStream_t s) {
+    if (interleaved)
+        norm_rope_write_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        norm_rope_write_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -173,7 +195,7 @@ extern "C" int ix_norm_rope_write_k(const void* k, int64_t k_stride, int dtype, 
     if (n < 0 || num_blocks < 0 || k_stride < 0 || max_pos < 0) return IX_ERR_SHAPE;
     const int es = dtype_bytes(dtype);
     if (!es || block_size != kBlock || !(eps >= 0.f) || !isfinite(eps)) return IX_ERR_UNSUPPORTED;
-    if (!(rot == 16 || (rot > 0 && rot % 32 == 0)) || offset < 0 || offset % 16 || offset + rot > kDim)
+    if (rot < 16 || rot % 16 || offset < 0 || offset % 8 || rot > kDim || offset > kDim - rot)
         return IX_ERR_UNSUPPORTED;
     if (n == 0) return IX_OK;
     if (!k || !gamma || !beta || !positions || !slot_mapping) return IX_ERR_NULL;
@@ -184,16 +206,16 @@ extern "C" int ix_norm_rope_write_k(const void* k, int64_t k_stride, int dtype, 
     int* st = status_ptr();
     const int sms = num_sms();
     if (!st || sms <= 0) return IX_ERR_CUDA;
-    const WriteArgs a{k, k_stride, n, gamma, beta, eps, positions, cos_sin, max_pos, rot, offset, interleaved ? 1 : 0,
+    const WriteArgs a{k, k_stride, n, gamma, beta, eps, positions, cos_sin, max_pos, rot, offset,
                       slot_mapping, cache, num_blocks, st};
-    const int64_t want = (n + kThreads / kLanes - 1) / (kThreads / kLanes), cap = static_cast<int64_t>(sms) * 8;
+    const int64_t want = (n + kThreads / kLanes - 1) / (kThreads / kLanes), cap = static_cast<int64_t>(sms) * 2;
     const int grid = static_cast<int>(want < cap ? want : cap);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == IX_BF16)
-        norm_rope_write_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+        launch<__nv_bfloat16>(a, interleaved, grid, s);
     else if (dtype == IX_FP16)
-        norm_rope_write_kernel<__half><<<grid, kThreads, 0, s>>>(a);
+        launch<__half>(a, interleaved, grid, s);
     else
-        norm_rope_write_kernel<float><<<grid, kThreads, 0, s>>>(a);
+        launch<float>(a, interleaved, grid, s);
     return launch_status();
 }
