@@ -1,18 +1,33 @@
 // norm.cuh -- what layer norm's forward and backward kernels share: how a row
-// lies over threads, sums over those threads, the weights.
+// lies over threads and in shared memory, sums over those threads, the weights.
 //
 // G threads hold a row, U vectors of V elements each: thread t has the vectors
-// t, t + G, t + 2G, ...  Up to 32 threads a row lies in (part of) a warp and is
-// summed by shuffles; beyond, a CTA holds one row.  The CTAs walk over the rows
-// of their own, and a thread loads its part of the next D rows before it sums
-// the present one, so that loads are always in flight behind the sums.
+// t, t + G, t + 2G, ...  What bounds these kernels beside DRAM is the issue of
+// instructions, and every thread of a row pays the row's sums, its root and its
+// addresses; so a thread has 32 elements where the row gives it as many, and the
+// arithmetic is in pairs (two f32 operations an instruction).  It holds the
+// weights of its columns in registers from row to row.
+//
+// The CTAs walk over rows of their own.  A thread copies its vectors of coming
+// rows into shared memory that it alone reads (16-byte asynchronous copies: no
+// barrier, no registers), so loads are in flight all the time.
+//
+// Rows of an odd width (kShift): where the tensors start on 16 bytes but their
+// rows do not, row r begins `shift` = r * stride mod V elements behind a 16-byte
+// boundary.  A grid whose step is a multiple of V rows gives every thread rows of
+// one and the same shift, so it still has columns of its own: its vectors start
+// at the boundary, its column c is that of the vector less the shift, and only
+// the first and the last vector of a row are cut.
 #pragma once
+
+#include <atomic>
+#include <initializer_list>
 
 #include "prep.cuh"
 
 namespace dsix {
 
-constexpr int kNarrowThreads = 256;  // a CTA of rows that lie within a warp
+constexpr int kNarrowThreads = 128;  // a CTA of rows that lie within a warp
 constexpr int kMaxCols = 32768;
 constexpr int kSms = 152;            // the grids' unit: whole multiples fill a GB300
 
@@ -23,11 +38,13 @@ struct RowShape {
     static constexpr int rows = narrow ? kNarrowThreads / G : 1;  // of a CTA at a time
 };
 
-// CTAs of so many threads that an SM holds at about so many registers a thread
-constexpr int ctas_per_sm(int threads, int regs) {
-    const int n = 65536 / (threads * ((regs + 7) / 8 * 8));
-    const int most = 2048 / threads;
-    return n < 1 ? 1 : n > most ? most : n;
+// CTAs of so many threads, registers a thread and bytes of shared memory that an SM holds
+constexpr int ctas_per_sm(int threads, int regs, int smem) {
+    const int by_regs = 65536 / (threads * ((regs + 7) / 8 * 8));
+    const int by_smem = smem ? 220 * 1024 / (smem + 2048) : 32;
+    const int by_threads = 2048 / threads;
+    const int n = by_regs < by_smem ? by_regs : by_smem;
+    return n < 1 ? 1 : n > by_threads ? by_threads : n;
 }
 
 // sums of N numbers over the G threads of a row; s: N * 32 floats of shared
@@ -55,19 +72,132 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[32]) {
     }
 }
 
-// V weights from column c on: f32, or of the activations' type
-template <class T, int V>
-__device__ __forceinline__ void load_weight(const void* w, bool f32, int c, float (&f)[V]) {
-    if (f32)
-        load_f32<V>(static_cast<const float*>(w) + c, f);
+// the first n of B bytes from global to shared memory, asynchronously, zeros behind them
+template <int B>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, uint32_t n) {
+    if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
     else
-        load_vec<T, V>(static_cast<const T*>(w) + c).unpack(f);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(B), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sums in pairs, of products too.  Vector u's elements go to partial sums in
+// turn, so that several independent additions are in flight; where a vector is a
+// single element, two vectors make a pair.
+template <int E>
+struct Pairs {
+    static constexpr int N = E >= 8 ? 4 : E >= 4 ? 2 : 1;
+    float2 p[N];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = make_float2(0.f, 0.f);
+    }
+    template <int V>
+    __device__ __forceinline__ void add(int u, const float (&f)[V]) {
+        if constexpr (V % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                float2& q = p[(u * (V / 2) + i) % N];
+                q = __fadd2_rn(q, make_float2(f[2 * i], f[2 * i + 1]));
+            }
+        } else {
+            float2& q = p[(u / 2) % N];
+            (u % 2 ? q.y : q.x) += f[0];
+        }
+    }
+    template <int V>
+    __device__ __forceinline__ void add_products(int u, const float (&f)[V], const float (&h)[V]) {
+        if constexpr (V % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                float2& q = p[(u * (V / 2) + i) % N];
+                q = __ffma2_rn(make_float2(f[2 * i], f[2 * i + 1]), make_float2(h[2 * i], h[2 * i + 1]), q);
+            }
+        } else {
+            float2& q = p[(u / 2) % N];
+            float& one = u % 2 ? q.y : q.x;
+            one = fmaf(f[0], h[0], one);
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        float2 s = p[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) s = __fadd2_rn(s, p[i]);
+        return s.x + s.y;
+    }
+};
+
+// Shared memory beyond kPlainSmem has to be asked for, once for each kernel and
+// device; rows in flight take at most kRowSmem.
+constexpr int kPlainSmem = 46 * 1024, kRowSmem = 200 * 1024;
+template <auto kernel>
+int allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return IX_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return IX_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return IX_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return IX_OK;
 }
 
 template <int V>
 __device__ __forceinline__ void fill(float (&f)[V], float v) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = v;
+}
+
+// V weights from column c on, which are f32 or of the activations' type; `none`
+// where there is no weight.  Under kShift c may be negative and need not be a
+// multiple of V.
+template <class T, int V, bool kShift>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int c, int cols, float none, float (&f)[V]) {
+    fill<V>(f, none);
+    if (!w || c >= cols) return;
+    if constexpr (kShift) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i >= 0 && c + i < cols)
+                f[i] = f32 ? __ldg(static_cast<const float*>(w) + c + i) : to_f32(static_cast<const T*>(w)[c + i]);
+    } else if (f32) {
+        load_f32<V>(static_cast<const float*>(w) + c, f);
+    } else {
+        load_vec<T, V>(static_cast<const T*>(w) + c).unpack(f);
+    }
+}
+
+// y to out[c .. c + V), without the columns that the row does not have
+template <class T, int V, bool kShift>
+__device__ __forceinline__ void store_row(T* out, int c, int cols, const Vec<T, V>& y) {
+    if (!kShift || (c >= 0 && c + V <= cols)) {
+        store_vec<T, V>(out + c, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i >= 0 && c + i < cols) out[c + i] = y.v[i];
+    }
+}
+
+// How a call's tensors lie: rows of whole 16-byte vectors, rows that start at
+// the same place behind a 16-byte boundary in every tensor, or neither.
+enum { kAligned, kShifted, kScattered };
+template <int W>
+int lie(int cols, std::initializer_list<const void*> bases, std::initializer_list<int64_t> strides) {
+    for (const void* p : bases)
+        if (!aligned16(p)) return kScattered;
+    bool whole = cols % W == 0;
+    for (int64_t s : strides) {
+        if (s % W != *strides.begin() % W) return kScattered;
+        whole = whole && s % W == 0;
+    }
+    return whole ? kAligned : kShifted;
 }
 
 }  // namespace dsix

@@ -23,115 +23,183 @@ struct BwdArgs {
 
 // CTAs that write column sums, at most: what their sums cost is bounded, also
 // where the columns are many
-constexpr int max_parts(int cols) { return kSms * (cols <= 2048 ? 4 : cols <= 4096 ? 3 : 2); }
+constexpr int max_parts(int cols) { return kSms * (cols <= 512 ? 8 : cols <= 2048 ? 4 : 2); }
 
-template <class T, int V, int G, int U, bool kSums>
+// the column sums of the row groups of a CTA: 32 elements of each thread
+constexpr int kGroupSmem = kNarrowThreads * 32 * sizeof(float);
+
+template <class T, int V, int G, int U>
 struct Bwd : RowShape<G> {
-    static constexpr int E = U * V, words = U * ((V * sizeof(T) + 3) / 4);
-    static constexpr bool hold = E <= 16 && V > 1 && G < 1024;
-    static constexpr int ahead = RowShape<G>::narrow && words <= 4 ? 2 : E <= 16 ? 1 : 0;
+    static constexpr int E = U * V, bytes = V * sizeof(T);
+    static constexpr bool hold = G <= 256;  // gamma stays in registers
+    static constexpr int slots = 2 * U;     // of a thread and stage: x, then dy
+    static constexpr int row = RowShape<G>::threads * slots * bytes;
+    // rows in shared memory: the present one, which both passes over it read
+    // there, and the next one on its way (one row where two would not fit; none
+    // where one would not: both passes then read global memory)
+    static constexpr int stages = kRowSmem / row < 2 ? kRowSmem / row : 2;
+    static constexpr bool async = bytes >= 4 && stages > 0;
+    static constexpr int rows_smem = async ? stages * row : 0;
+    static constexpr int smem = RowShape<G>::narrow && rows_smem < kGroupSmem ? kGroupSmem : rows_smem;
     // the same shape with and without the column sums
-    static constexpr int ctas =
-        ctas_per_sm(RowShape<G>::threads, 2 * E + (hold ? E : 0) + (ahead + 1) * 2 * words + 32);
+    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, 2 * E + (hold ? E : 0) + 56, smem);
 };
 
-template <class T, int V, int G, int U, bool kSums>
-__global__ void __launch_bounds__(Bwd<T, V, G, U, kSums>::threads, Bwd<T, V, G, U, kSums>::ctas)
-    norm_bwd_kernel(const BwdArgs a) {
-    using F = Bwd<T, V, G, U, kSums>;
+template <class T, int V, int G, int U, bool kSums, bool kShift>
+__global__ void __launch_bounds__(Bwd<T, V, G, U>::threads, Bwd<T, V, G, U>::ctas) norm_bwd_kernel(const BwdArgs a) {
+    using F = Bwd<T, V, G, U>;
+    extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ float s_sum[2][2][32];
     const int t = threadIdx.x % G, sub = threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * F::rows;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * F::rows;
-    struct Row {
-        Vec<T, V> x[U], dy[U];
-        float mean, rstd;
-    };
-    // a row past the end has dy = x = 0 and mean = rstd = 0: it adds nothing
-    auto load = [&](Row& r, int64_t row) {
-        const bool live = row < a.rows;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * F::rows;
+    const int shift = kShift ? static_cast<int>((r0 + sub) * a.x_stride % V) : 0;
+    const int c0 = t * V - shift;  // vector u begins with column c0 + u * G * V
+    Vec<T, V>* slot = reinterpret_cast<Vec<T, V>*>(s_rows) + threadIdx.x;  // this thread's, F::threads apart
+    auto fetch = [&](int64_t row, int stage) {
         const T* px = static_cast<const T*>(a.x) + row * a.x_stride;
         const T* pd = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        Vec<T, V>* to = slot + stage * F::slots * F::threads;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (u * G + t) * V;
-            r.x[u] = live && c < a.cols ? load_vec<T, V>(px + c) : zero_vec<T, V>();
-            r.dy[u] = live && c < a.cols ? load_vec<T, V>(pd + c) : zero_vec<T, V>();
+            const int c = c0 + u * G * V;
+            const bool live = row < a.rows && c < a.cols;
+            const uint32_t n = !live ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
+            copy_async<F::bytes>(to + u * F::threads, live ? px + c : a.x, n);
+            copy_async<F::bytes>(to + (U + u) * F::threads, live ? pd + c : a.dy, n);
         }
-        r.mean = live ? __ldg(a.mean + row) : 0.f;
-        r.rstd = live ? __ldg(a.rstd + row) : 0.f;
+        copy_commit();
     };
-    auto weight = [&](float(&w)[V], int c) {
-        fill<V>(w, 1.f);
-        if (a.gamma && c < a.cols) load_weight<T, V>(a.gamma, a.weight_f32, c, w);
-    };
-    Row ring[F::ahead + 1];
-#pragma unroll
-    for (int k = 0; k <= F::ahead; ++k) load(ring[k], row0 + k * step + sub);
+    auto stat = [&](const float* p, int64_t row) { return row < a.rows ? __ldg(p + row) : 0.f; };
+    if constexpr (F::async) {
+        for (int k = 0; k < F::stages; ++k) fetch(r0 + sub + k * step, k);
+    }
+    float mean = stat(a.mean, r0 + sub), rstd = stat(a.rstd, r0 + sub);
     float ag[kSums ? F::E : 1], ab[kSums ? F::E : 1], g[F::hold ? U : 1][V];
     if constexpr (kSums) {
         fill<F::E>(ag, 0.f);
         fill<F::E>(ab, 0.f);
     }
+    auto weight = [&](int u, int c) { load_weight<T, V, kShift>(a.gamma, a.weight_f32, c, a.cols, 1.f, g[u]); };
     if constexpr (F::hold) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) weight(g[u], (u * G + t) * V);
+        for (int u = 0; u < U; ++u) weight(u, c0 + u * G * V);
     }
-    int flip = 0;  // the sums of consecutive rows use other places: one barrier a row is enough
-    for (int64_t r0 = row0; r0 < a.rows; r0 += step) {
-        const Row& r = ring[0];
+    int stage = 0, flip = 0;  // the sums of consecutive rows use other places: one barrier a row is enough
+    for (; r0 < a.rows; r0 += step) {
         const int64_t row = r0 + sub;
-        float sums[2] = {0.f, 0.f};  // of h and h * xhat
-        // roundings spelled out: with and without the column sums, dx has the same bits
+        const bool live = row < a.rows;
+        Vec<T, V>* from = slot + stage * F::slots * F::threads;
+        const T* px = static_cast<const T*>(a.x) + row * a.x_stride;
+        const T* pd = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        // vector u of x and dy; zeros outside of the row, where they add nothing: dy = 0, and
+        // for a row past the last x = mean = rstd = 0 too
+        auto read = [&](int u, float(&x)[V], float(&d)[V]) {
+            if constexpr (F::async) {
+                from[u * F::threads].unpack(x);
+                from[(U + u) * F::threads].unpack(d);
+            } else {
+                const int c = c0 + u * G * V;
+                (live && c < a.cols ? load_vec<T, V>(px + c) : zero_vec<T, V>()).unpack(x);
+                (live && c < a.cols ? load_vec<T, V>(pd + c) : zero_vec<T, V>()).unpack(d);
+            }
+        };
+        if constexpr (F::async) copy_wait<F::stages - 1>();
+        if (kShift && t == 0) {  // what lies before the row
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = (u * G + t) * V;
-            if constexpr (!F::hold) weight(g[0], c);
-            if (c < a.cols) {
-                float x[V], d[V];
-                r.x[u].unpack(x);
-                r.dy[u].unpack(d);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = __fmul_rn(__fsub_rn(x[i], r.mean), r.rstd);
-                    const float h = __fmul_rn(d[i], g[F::hold ? u : 0][i]);
-                    sums[0] = __fadd_rn(sums[0], h);
-                    sums[1] = fmaf(h, xh, sums[1]);
-                    if constexpr (kSums) {
-                        ag[u * V + i] = fmaf(d[i], xh, ag[u * V + i]);
-                        ab[u * V + i] += d[i];
-                    }
+            for (int i = 0; i < V - 1; ++i) {
+                if (i < shift) {
+                    from_f32(0.f, from[0].v[i]);
+                    from_f32(0.f, from[U * F::threads].v[i]);
                 }
             }
         }
+        const float mean_next = stat(a.mean, row + step), rstd_next = stat(a.rstd, row + step);
+        Pairs<F::E> sh, shx;  // of h and h * xhat
+        sh.clear();
+        shx.clear();
+        const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+        constexpr int keep = F::hold;
+        // (without a test of the column: outside of the row dy = 0)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (!F::hold) weight(0, c0 + u * G * V);
+            const float(&w)[V] = g[u * keep];
+            float x[V], d[V], h[V];
+            read(u, x, d);
+            if constexpr (V % 2 == 0) {
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 xh = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), m2), r2);
+                    const float2 d2 = make_float2(d[i], d[i + 1]);
+                    const float2 h2 = __fmul2_rn(d2, make_float2(w[i], w[i + 1]));
+                    x[i] = xh.x;
+                    x[i + 1] = xh.y;
+                    h[i] = h2.x;
+                    h[i + 1] = h2.y;
+                    if constexpr (kSums) {
+                        const int k = u * V + i;
+                        const float2 g2 = __ffma2_rn(d2, xh, make_float2(ag[k], ag[k + 1]));
+                        const float2 b2 = __fadd2_rn(d2, make_float2(ab[k], ab[k + 1]));
+                        ag[k] = g2.x;
+                        ag[k + 1] = g2.y;
+                        ab[k] = b2.x;
+                        ab[k + 1] = b2.y;
+                    }
+                }
+            } else {
+                // roundings spelled out: with and without the column sums, dx has the same bits
+                x[0] = __fmul_rn(__fsub_rn(x[0], mean), rstd);
+                h[0] = __fmul_rn(d[0], w[0]);
+                if constexpr (kSums) {
+                    ag[u] = fmaf(d[0], x[0], ag[u]);
+                    ab[u] += d[0];
+                }
+            }
+            sh.template add<V>(u, h);
+            shx.template add_products<V>(u, h, x);
+        }
+        float sums[2] = {sh.total(), shx.total()};
         row_sums<G>(sums, s_sum[flip]);
-        flip ^= 1;
-        if (row < a.rows) {
+        if (live) {
             const float mh = __fmul_rn(sums[0], a.inv_cols), mhx = __fmul_rn(sums[1], a.inv_cols);
             T* out = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = (u * G + t) * V;
-                if constexpr (!F::hold) weight(g[0], c);
-                if (c < a.cols) {
-                    float x[V], d[V];
-                    r.x[u].unpack(x);
-                    r.dy[u].unpack(d);
+                const int c = c0 + u * G * V;
+                if constexpr (!F::hold) weight(0, c);
+                const float(&w)[V] = g[u * keep];
+                float x[V], d[V];
+                read(u, x, d);
+                // dx = rstd * ((h - mh) - xhat * mhx)
+                if constexpr (V % 2 == 0) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float xh = __fmul_rn(__fsub_rn(x[i], r.mean), r.rstd);
-                        const float h = __fmul_rn(d[i], g[F::hold ? u : 0][i]);
-                        d[i] = __fmul_rn(r.rstd, fmaf(-xh, mhx, __fsub_rn(h, mh)));
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 xh = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), m2), r2);
+                        const float2 h2 = __fmul2_rn(make_float2(d[i], d[i + 1]), make_float2(w[i], w[i + 1]));
+                        float2 y = __fadd2_rn(h2, make_float2(-mh, -mh));
+                        y = __ffma2_rn(xh, make_float2(-mhx, -mhx), y);
+                        y = __fmul2_rn(y, r2);
+                        d[i] = y.x;
+                        d[i + 1] = y.y;
                     }
-                    Vec<T, V> y;
-                    y.pack(d);
-                    store_vec<T, V>(out + c, y);
+                } else {
+                    const float xh = __fmul_rn(__fsub_rn(x[0], mean), rstd);
+                    const float h = __fmul_rn(d[0], w[0]);
+                    d[0] = __fmul_rn(rstd, fmaf(-xh, mhx, __fsub_rn(h, mh)));
                 }
+                Vec<T, V> y;
+                y.pack(d);
+                if (c < a.cols) store_row<T, V, kShift>(out, c, a.cols, y);
             }
         }
-#pragma unroll
-        for (int k = 0; k < F::ahead; ++k) ring[k] = ring[k + 1];
-        load(ring[F::ahead], row + (F::ahead + 1) * step);
+        if constexpr (F::async) {
+            fetch(row + F::stages * step, stage);  // this thread has read the stage
+            stage = stage + 1 == F::stages ? 0 : stage + 1;
+        }
+        flip ^= 1;
+        mean = mean_next;
+        rstd = rstd_next;
     }
     if constexpr (kSums) {
         float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
@@ -140,17 +208,19 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U, kSums>::threads, Bwd<T, V, G, 
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int c = (u * G + t) * V + i;
-                    if (c < a.cols) {
+                    const int c = c0 + u * G * V + i;
+                    if (c >= 0 && c < a.cols) {
                         part[c] = ag[u * V + i];
                         part[a.cols + c] = ab[u * V + i];
                     }
                 }
         } else {
-            // the CTA's row groups: those of a warp by shuffles, the warps in shared memory
-            constexpr int kWarps = F::threads / 32, kCols = G * U * V;
-            __shared__ float s_part[kWarps][kCols];
-            const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+            // the CTA's row groups, whose columns may lie apart by their shifts, meet in
+            // the shared memory of the rows, in the groups' order
+            constexpr int kCols = G * U * V;
+            static_assert(F::rows * kCols * static_cast<int>(sizeof(float)) <= kGroupSmem, "");
+            float* s_part = reinterpret_cast<float*>(s_rows);
+            if constexpr (F::async) copy_wait<0>();
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 __syncthreads();
@@ -158,16 +228,14 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U, kSums>::threads, Bwd<T, V, G, 
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        float v = w ? ab[u * V + i] : ag[u * V + i];
-#pragma unroll
-                        for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                        if (lane < G) s_part[warp][(u * G + t) * V + i] = v;
+                        const int c = c0 + u * G * V + i;
+                        if (c >= 0 && c < a.cols) s_part[sub * kCols + c] = w ? ab[u * V + i] : ag[u * V + i];
                     }
                 __syncthreads();
                 for (int c = threadIdx.x; c < a.cols; c += F::threads) {
                     float v = 0.f;
 #pragma unroll
-                    for (int k = 0; k < kWarps; ++k) v += s_part[k][c];
+                    for (int k = 0; k < F::rows; ++k) v += s_part[k * kCols + c];
                     part[w * a.cols + c] = v;
                 }
             }
@@ -219,41 +287,54 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int
     }
 }
 
-template <class T, int V, int G, int U, bool kSums>
+template <class T, int V, int G, int U, bool kSums, bool kShift = false>
 int launch(const BwdArgs& a, int* parts, cudaStream_t s) {
-    using F = Bwd<T, V, G, U, kSums>;
-    const int64_t want = (a.rows + F::rows - 1) / F::rows;
-    const int cap = max_parts(a.cols), most = kSms * F::ctas < cap ? kSms * F::ctas : cap;
+    using F = Bwd<T, V, G, U>;
+    static_assert(!kShift || F::async, "the first vector is cut in shared memory");
+    int64_t want = (a.rows + F::rows - 1) / F::rows;
+    if (kShift) want = (want + V - 1) / V * V;  // CTAs without a row write zero sums
+    const int cap = max_parts(a.cols), most = kSms * F::ctas < cap ? kSms * F::ctas : cap;  // multiples of V
     const int grid = static_cast<int>(want < most ? want : most);
     if (kSums) *parts = grid;
-    norm_bwd_kernel<T, V, G, U, kSums><<<grid, F::threads, 0, s>>>(a);
+    if constexpr (F::smem > kPlainSmem) {
+        const int rc = allow_smem<norm_bwd_kernel<T, V, G, U, kSums, kShift>>(F::smem);
+        if (rc != IX_OK) return rc;
+    }
+    norm_bwd_kernel<T, V, G, U, kSums, kShift><<<grid, F::threads, F::smem, s>>>(a);
     return launch_status();
 }
 
+constexpr int kFusedCols = 16384, kFusedScattered = 8192;  // with column sums
+
+// 32 elements a thread, fewer where the row is short
+template <class T, bool kSums, bool kShift>
+int by_width(const BwdArgs& a, int* parts, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T), U = 32 / W;
+    const int n = a.cols + (kShift ? W - 1 : 0);
+    if (n <= 64) return launch<T, W, 8, U / 4, kSums, kShift>(a, parts, s);
+    if (n <= 128) return launch<T, W, 8, U / 2, kSums, kShift>(a, parts, s);
+    if (n <= 256) return launch<T, W, 8, U, kSums, kShift>(a, parts, s);
+    if (n <= 512) return launch<T, W, 16, U, kSums, kShift>(a, parts, s);
+    if (n <= 1024) return launch<T, W, 32, U, kSums, kShift>(a, parts, s);
+    if (n <= 2048) return launch<T, W, 64, U, kSums, kShift>(a, parts, s);
+    if (n <= 4096) return launch<T, W, 128, U, kSums, kShift>(a, parts, s);
+    if (n <= 8192) return launch<T, W, 256, U, kSums, kShift>(a, parts, s);
+    if (n <= kFusedCols) return launch<T, W, 512, U, kSums, kShift>(a, parts, s);
+    if constexpr (!kSums && !kShift) return launch<T, W, 1024, U, false>(a, parts, s);
+    if constexpr (!kSums && kShift) return launch<T, 1, 1024, 32, false>(a, parts, s);
+    return IX_ERR_UNSUPPORTED;
+}
+
 template <class T, bool kSums>
-int fused(const BwdArgs& a, bool wide, int* parts, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T);
-    if (wide) {
-        const int n = a.cols / W;
-        if (n <= 16) return launch<T, W, 16, 1, kSums>(a, parts, s);
-        if (n <= 32) return launch<T, W, 32, 1, kSums>(a, parts, s);
-        if (n <= 64) return launch<T, W, 32, 2, kSums>(a, parts, s);
-        if (n <= 256) return launch<T, W, 256, 1, kSums>(a, parts, s);
-        if (n <= 512) return launch<T, W, 256, 2, kSums>(a, parts, s);
-        if (n <= 1024) return launch<T, W, 512, 2, kSums>(a, parts, s);
-        if (n <= 2048) return launch<T, W, 512, 4, kSums>(a, parts, s);
-        if constexpr (!kSums) {
-            if (n <= 4096) return launch<T, W, 1024, 4, false>(a, parts, s);
-            if constexpr (W == 4) return launch<T, W, 1024, 8, false>(a, parts, s);
-        }
-        return IX_ERR_UNSUPPORTED;
-    }
+int fused(const BwdArgs& a, int how, int* parts, cudaStream_t s) {
+    if (how == kAligned) return by_width<T, kSums, false>(a, parts, s);
+    if (how == kShifted) return by_width<T, kSums, true>(a, parts, s);
+    // an element at a time
     const int n = a.cols;
-    if (n <= 32) return launch<T, 1, 32, 1, kSums>(a, parts, s);
     if (n <= 128) return launch<T, 1, 32, 4, kSums>(a, parts, s);
-    if (n <= 512) return launch<T, 1, 128, 4, kSums>(a, parts, s);
-    if (n <= 2048) return launch<T, 1, 256, 8, kSums>(a, parts, s);
-    if (n <= 8192) return launch<T, 1, 512, 16, kSums>(a, parts, s);
+    if (n <= 512) return launch<T, 1, 32, 16, kSums>(a, parts, s);
+    if (n <= 2048) return launch<T, 1, 128, 16, kSums>(a, parts, s);
+    if (n <= kFusedScattered) return launch<T, 1, 512, 16, kSums>(a, parts, s);
     if constexpr (!kSums) return launch<T, 1, 1024, 32, false>(a, parts, s);
     return IX_ERR_UNSUPPORTED;
 }
@@ -263,17 +344,17 @@ int dispatch(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T);
     int parts = 0, rc = IX_OK;
     if (a.rows > 0) {
-        const bool wide = a.cols % W == 0 && a.x_stride % W == 0 && a.dy_stride % W == 0 && a.dx_stride % W == 0 &&
-                          aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx);
-        if (!dgamma) return fused<T, false>(a, wide, nullptr, s);
-        if (a.cols <= (wide ? 2048 * W : 8192)) {
-            rc = fused<T, true>(a, wide, &parts, s);
+        const int how = lie<W>(a.cols, {a.x, a.dy, a.dx}, {a.x_stride, a.dy_stride, a.dx_stride});
+        if (!dgamma) return fused<T, false>(a, how, nullptr, s);
+        const int most = how == kScattered ? kFusedScattered : kFusedCols - (how == kShifted ? W - 1 : 0);
+        if (a.cols <= most) {
+            rc = fused<T, true>(a, how, &parts, s);
         } else {
             // before dx is written: dx may be dy in place
             parts = static_cast<int>(a.rows < max_parts(a.cols) ? a.rows : max_parts(a.cols));
             norm_cols_kernel<T><<<dim3((a.cols + kColThreads - 1) / kColThreads, parts), kColThreads, 0, s>>>(a);
             rc = launch_status();
-            if (rc == IX_OK) rc = fused<T, false>(a, wide, nullptr, s);
+            if (rc == IX_OK) rc = fused<T, false>(a, how, nullptr, s);
         }
         if (rc != IX_OK) return rc;
     }
@@ -289,8 +370,9 @@ using namespace dsix;
 
 extern "C" size_t ix_layer_norm_bwd_workspace_size(int64_t rows, int cols) {
     if (rows <= 0 || cols <= 0) return 0;
-    const int most = max_parts(cols);
-    return static_cast<size_t>(rows < most ? rows : most) * 2 * static_cast<size_t>(cols) * sizeof(float);
+    // rows of an odd width may take some CTAs more than there are rows
+    const int64_t parts = rows + 8 < max_parts(cols) ? rows + 8 : max_parts(cols);
+    return static_cast<size_t>(parts) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 
 extern "C" int ix_layer_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

@@ -1,8 +1,8 @@
 // norm_fwd.cu -- ix_layer_norm.
 //
-// The row is read once and stays in registers, as it came, for the three passes
-// over it: the sum, the sum of the centred squares (no cancellation, whatever
-// the mean), the output.
+// The row is copied to shared memory once and read there by the three passes over
+// it: the sum, the sum of the centred squares (no cancellation, whatever the
+// mean), the output.
 #include "norm.cuh"
 
 namespace dsix {
@@ -20,73 +20,112 @@ struct NormArgs {
 
 template <class T, int V, int G, int U>
 struct Fwd : RowShape<G> {
-    static constexpr int E = U * V, words = U * ((V * sizeof(T) + 3) / 4);
-    // the weights stay in registers where a thread has few columns
-    static constexpr bool hold = E <= 16 && V > 1 && G < 1024;
-    static constexpr int ahead = RowShape<G>::narrow && words <= 4 ? 3 : E <= 16 ? 1 : 0;
-    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, (hold ? 2 * E : 0) + (ahead + 1) * words + 36);
+    static constexpr int E = U * V, bytes = V * sizeof(T), row = RowShape<G>::threads * U * bytes;
+    // the weights stay in registers, as long as the threads of the widest rows have them
+    static constexpr bool hold = G < 1024;
+    // rows in shared memory: the present one and the next ones on their way
+    static constexpr int stages = kRowSmem / row < 3 ? kRowSmem / row : 3;
+    static constexpr bool async = bytes >= 4 && stages > 0;
+    static constexpr int smem = async ? stages * row : 0;
+    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, (hold ? 2 * E : 0) + 56, smem);
 };
 
-template <class T, int V, int G, int U>
+template <class T, int V, int G, int U, bool kShift>
 __global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::ctas) norm_fwd_kernel(const NormArgs a) {
     using F = Fwd<T, V, G, U>;
+    extern __shared__ __align__(16) uint8_t s_row[];
     __shared__ float s_sum[4][1][32];
-    const int t = threadIdx.x % G;
+    const int t = threadIdx.x % G, sub = threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * F::rows;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * F::rows;
-    const int sub = threadIdx.x / G;
-    auto load = [&](Vec<T, V>(&x)[U], int64_t row) {
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * F::rows;
+    const int shift = kShift ? static_cast<int>((r0 + sub) * a.x_stride % V) : 0;
+    const int c0 = t * V - shift;  // vector u begins with column c0 + u * G * V
+    Vec<T, V>* slot = reinterpret_cast<Vec<T, V>*>(s_row) + threadIdx.x;  // this thread's, F::threads apart
+    auto fetch = [&](int64_t row, int stage) {
         const T* in = static_cast<const T*>(a.x) + row * a.x_stride;
+        Vec<T, V>* to = slot + stage * U * F::threads;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = (u * G + t) * V;
-            x[u] = row < a.rows && c < a.cols ? load_vec<T, V>(in + c) : zero_vec<T, V>();
+            const int c = c0 + u * G * V;
+            const bool live = row < a.rows && c < a.cols;
+            const uint32_t n = !live ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
+            copy_async<F::bytes>(to + u * F::threads, live ? in + c : a.x, n);
         }
+        copy_commit();
     };
-    Vec<T, V> ring[F::ahead + 1][U];  // the present row and the next ones
-#pragma unroll
-    for (int k = 0; k <= F::ahead; ++k) load(ring[k], row0 + k * step + sub);
+    if constexpr (F::async) {
+        for (int k = 0; k < F::stages; ++k) fetch(r0 + sub + k * step, k);
+    }
     float g[F::hold ? U : 1][V], b[F::hold ? U : 1][V];
-    auto weights = [&](float(&gv)[V], float(&bv)[V], int c) {
-        fill<V>(gv, 1.f);
-        fill<V>(bv, 0.f);
-        if (c < a.cols) {
-            if (a.gamma) load_weight<T, V>(a.gamma, a.weight_f32, c, gv);
-            if (a.beta) load_weight<T, V>(a.beta, a.weight_f32, c, bv);
-        }
+    auto weights = [&](int u, int c) {
+        load_weight<T, V, kShift>(a.gamma, a.weight_f32, c, a.cols, 1.f, g[u]);
+        load_weight<T, V, kShift>(a.beta, a.weight_f32, c, a.cols, 0.f, b[u]);
     };
     if constexpr (F::hold) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) weights(g[u], b[u], (u * G + t) * V);
+        for (int u = 0; u < U; ++u) weights(u, c0 + u * G * V);
     }
-    int flip = 0;  // the sums of consecutive rows use other places: one barrier a sum is enough
-    for (int64_t r0 = row0; r0 < a.rows; r0 += step) {
-        Vec<T, V>(&x)[U] = ring[0];
+    int stage = 0, flip = 0;  // the sums of consecutive rows use other places: one barrier a sum is enough
+    for (; r0 < a.rows; r0 += step) {
         const int64_t row = r0 + sub;
-        float sum[1] = {0.f};
+        const bool live = row < a.rows;
+        Vec<T, V>* from = slot + stage * U * F::threads;
+        const T* in = static_cast<const T*>(a.x) + row * a.x_stride;
+        // vector u of the row, zeros past its end and for a row past the last
+        auto read = [&](int u, float(&f)[V]) {
+            if constexpr (F::async) {
+                from[u * F::threads].unpack(f);
+            } else {
+                const int c = c0 + u * G * V;
+                (live && c < a.cols ? load_vec<T, V>(in + c) : zero_vec<T, V>()).unpack(f);
+            }
+        };
+        if constexpr (F::async) copy_wait<F::stages - 1>();
+        if (kShift && t == 0) {  // what lies before the row
+#pragma unroll
+            for (int i = 0; i < V - 1; ++i)
+                if (i < shift) from_f32(0.f, from[0].v[i]);
+        }
+        Pairs<F::E> sum;
+        sum.clear();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[V];
-            x[u].unpack(f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[0] += f[i];
+            read(u, f);
+            sum.template add<V>(u, f);
         }
-        row_sums<G>(sum, s_sum[2 * flip]);
-        const float mean = sum[0] * a.inv_cols;
-        float sq[1] = {0.f};
+        float total[1] = {sum.total()};
+        row_sums<G>(total, s_sum[2 * flip]);
+        const float mean = total[0] * a.inv_cols;
+        sum.clear();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if ((u * G + t) * V < a.cols) {
+            const int c = c0 + u * G * V;
+            if (c < a.cols) {
                 float f[V];
-                x[u].unpack(f);
+                read(u, f);
+                if constexpr (V % 2 == 0) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) sq[0] = fmaf(f[i] - mean, f[i] - mean, sq[0]);
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 d = __fadd2_rn(make_float2(f[i], f[i + 1]), make_float2(-mean, -mean));
+                        f[i] = d.x;
+                        f[i + 1] = d.y;
+                    }
+                } else {
+                    f[0] -= mean;
+                }
+                if (kShift && (c < 0 || c + V > a.cols)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (c + i < 0 || c + i >= a.cols) f[i] = 0.f;
+                }
+                sum.template add_products<V>(u, f, f);
             }
         }
+        float sq[1] = {sum.total()};
         row_sums<G>(sq, s_sum[2 * flip + 1]);
-        flip ^= 1;
-        const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sq[0], a.inv_cols, a.eps)));
-        if (row < a.rows) {
+        const float rstd = rsqrtf(fmaf(sq[0], a.inv_cols, a.eps));
+        if (live) {
             if (t == 0 && a.mean) {
                 a.mean[row] = mean;
                 a.rstd[row] = rstd;
@@ -94,61 +133,81 @@ __global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::cta
             T* out = static_cast<T*>(a.out) + row * a.out_stride;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = (u * G + t) * V;
-                if constexpr (!F::hold) weights(g[0], b[0], c);
+                const int c = c0 + u * G * V;
                 if (c < a.cols) {
+                    constexpr int keep = F::hold;
+                    if constexpr (!F::hold) weights(0, c);
                     float f[V];
-                    x[u].unpack(f);
+                    read(u, f);
+                    if constexpr (V % 2 == 0) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        f[i] = fmaf((f[i] - mean) * rstd, g[F::hold ? u : 0][i], b[F::hold ? u : 0][i]);
+                        for (int i = 0; i < V; i += 2) {
+                            float2 y = __fadd2_rn(make_float2(f[i], f[i + 1]), make_float2(-mean, -mean));
+                            y = __fmul2_rn(y, make_float2(rstd, rstd));
+                            y = __ffma2_rn(y, make_float2(g[u * keep][i], g[u * keep][i + 1]),
+                                           make_float2(b[u * keep][i], b[u * keep][i + 1]));
+                            f[i] = y.x;
+                            f[i + 1] = y.y;
+                        }
+                    } else {
+                        f[0] = fmaf((f[0] - mean) * rstd, g[u * keep][0], b[u * keep][0]);
+                    }
                     Vec<T, V> y;
                     y.pack(f);
-                    store_vec<T, V>(out + c, y);
+                    store_row<T, V, kShift>(out, c, a.cols, y);
                 }
             }
         }
-#pragma unroll
-        for (int k = 0; k < F::ahead; ++k)
-#pragma unroll
-            for (int u = 0; u < U; ++u) ring[k][u] = ring[k + 1][u];
-        load(ring[F::ahead], row + (F::ahead + 1) * step);
+        if constexpr (F::async) {
+            fetch(row + F::stages * step, stage);  // this thread has read the stage
+            stage = stage + 1 == F::stages ? 0 : stage + 1;
+        }
+        flip ^= 1;
     }
 }
 
-template <class T, int V, int G, int U>
+template <class T, int V, int G, int U, bool kShift = false>
 int launch(const NormArgs& a, cudaStream_t s) {
     using F = Fwd<T, V, G, U>;
-    const int64_t want = (a.rows + F::rows - 1) / F::rows, most = kSms * F::ctas;
-    norm_fwd_kernel<T, V, G, U><<<static_cast<int>(want < most ? want : most), F::threads, 0, s>>>(a);
+    static_assert(!kShift || F::async, "the first vector is cut in shared memory");
+    int64_t want = (a.rows + F::rows - 1) / F::rows;
+    const int64_t most = kSms * F::ctas;  // a multiple of V
+    if (kShift) want = (want + V - 1) / V * V;
+    if constexpr (F::smem > kPlainSmem) {
+        const int rc = allow_smem<norm_fwd_kernel<T, V, G, U, kShift>>(F::smem);
+        if (rc != IX_OK) return rc;
+    }
+    norm_fwd_kernel<T, V, G, U, kShift><<<static_cast<int>(want < most ? want : most), F::threads, F::smem, s>>>(a);
     return launch_status();
+}
+
+// 32 elements a thread, fewer where the row is short
+template <class T, bool kShift>
+int by_width(const NormArgs& a, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(T), U = 32 / W;
+    const int n = a.cols + (kShift ? W - 1 : 0);
+    if (n <= 64) return launch<T, W, 8, U / 4, kShift>(a, s);
+    if (n <= 128) return launch<T, W, 8, U / 2, kShift>(a, s);
+    if (n <= 256) return launch<T, W, 8, U, kShift>(a, s);
+    if (n <= 512) return launch<T, W, 16, U, kShift>(a, s);
+    if (n <= 1024) return launch<T, W, 32, U, kShift>(a, s);
+    if (n <= 2048) return launch<T, W, 64, U, kShift>(a, s);
+    if (n <= 4096) return launch<T, W, 128, U, kShift>(a, s);
+    if (n <= 8192) return launch<T, W, 256, U, kShift>(a, s);
+    if (n <= 16384) return launch<T, W, 512, U, kShift>(a, s);
+    return launch<T, W, 1024, U + (kShift ? 1 : 0), kShift>(a, s);
 }
 
 template <class T>
 int dispatch(const NormArgs& a, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T);
-    const bool wide = a.cols % W == 0 && a.x_stride % W == 0 && a.out_stride % W == 0 && aligned16(a.x) &&
-                      aligned16(a.out);
-    if (wide) {
-        const int n = a.cols / W;
-        if (n <= 16) return launch<T, W, 16, 1>(a, s);
-        if (n <= 32) return launch<T, W, 32, 1>(a, s);
-        if (n <= 64) return launch<T, W, 32, 2>(a, s);
-        if (n <= 128) return launch<T, W, 64, 2>(a, s);
-        if (n <= 256) return launch<T, W, 128, 2>(a, s);
-        if (n <= 512) return launch<T, W, 256, 2>(a, s);
-        if (n <= 1024) return launch<T, W, 512, 2>(a, s);
-        if (n <= 2048) return launch<T, W, 1024, 2>(a, s);
-        if (n <= 4096) return launch<T, W, 1024, 4>(a, s);
-        if constexpr (W == 4) return launch<T, W, 1024, 8>(a, s);
-        return IX_ERR_UNSUPPORTED;
-    }
+    const int how = lie<16 / sizeof(T)>(a.cols, {a.x, a.out}, {a.x_stride, a.out_stride});
+    if (how == kAligned) return by_width<T, false>(a, s);
+    if (how == kShifted) return by_width<T, true>(a, s);
+    // an element at a time
     const int n = a.cols;
-    if (n <= 32) return launch<T, 1, 32, 1>(a, s);
     if (n <= 128) return launch<T, 1, 32, 4>(a, s);
-    if (n <= 512) return launch<T, 1, 64, 8>(a, s);
-    if (n <= 2048) return launch<T, 1, 256, 8>(a, s);
-    if (n <= 8192) return launch<T, 1, 512, 16>(a, s);
+    if (n <= 1024) return launch<T, 1, 32, 32>(a, s);
+    if (n <= 4096) return launch<T, 1, 128, 32>(a, s);
     return launch<T, 1, 1024, 32>(a, s);
 }
 

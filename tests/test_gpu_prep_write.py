@@ -73,7 +73,7 @@ def entries(cache):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("rot,offset", [(64, 0), (64, 64), (32, 0), (32, 48), (16, 0), (16, 112), (96, 16), (128, 0)])
+@pytest.mark.parametrize("rot,offset", [(64, 0), (64, 64), (32, 0), (32, 48), (16, 0), (16, 112), (96, 16), (48, 8), (128, 0)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_values(dsix, dtype, rot, offset, interleaved):
     for n, pad, skip in ((1, 0, 0), (2, 16, 0), (63, 64, 5), (1000, 0, 3)):

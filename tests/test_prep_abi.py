@@ -116,6 +116,7 @@ def test_rope_table_refusals(lib):
     assert lib.ix_rope_table(f, 64, 2 ** 62, 2 ** 62, 1.0, A, None) == UNSUPPORTED
     assert lib.ix_rope_table(f, 64, 0, 4, float("inf"), A, None) == UNSUPPORTED
     assert lib.ix_rope_table(bad, 64, 0, 4, 1.0, A, None) == UNSUPPORTED
+    assert lib.ix_rope_table((ctypes.c_double * 32)(*[2.0 ** 20] * 32), 64, 0, 4, 1.0, A, None) == UNSUPPORTED
     assert lib.ix_rope_table(None, 64, 0, 4, 1.0, A, None) == NULL
     assert lib.ix_rope_table(f, 64, 0, 4, 1.0, None, None) == NULL
     assert lib.ix_rope_table(f, 64, 0, 4, 1.0, P(0x10008), None) == ALIGN
@@ -178,8 +179,8 @@ def _write(**kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(n=-1), SHAPE), (dict(nb=-1), SHAPE), (dict(ks=-128), SHAPE), (dict(max_pos=-1), SHAPE),
     (dict(dtype=4), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(eps=-1.0), UNSUPPORTED),
-    (dict(rot=0), UNSUPPORTED), (dict(rot=48), UNSUPPORTED), (dict(rot=8), UNSUPPORTED), (dict(off=8), UNSUPPORTED),
-    (dict(off=80), UNSUPPORTED), (dict(off=-16), UNSUPPORTED), (dict(k=None), NULL), (dict(gamma=None), NULL),
+    (dict(rot=0), UNSUPPORTED), (dict(rot=40), UNSUPPORTED), (dict(rot=8), UNSUPPORTED), (dict(off=4), UNSUPPORTED),
+    (dict(off=72), UNSUPPORTED), (dict(rot=144), UNSUPPORTED), (dict(off=-16), UNSUPPORTED), (dict(k=None), NULL), (dict(gamma=None), NULL),
     (dict(slots=None), NULL), (dict(table=None), NULL), (dict(cache=None), NULL), (dict(ks=132), ALIGN),
     (dict(k=P(0x10008)), ALIGN), (dict(table=P(0x10004)), ALIGN), (dict(pos=P(0x10004)), ALIGN), (dict(n=0), OK),
 ])
