@@ -2,11 +2,12 @@
 // lies over threads and in shared memory, sums over those threads, the weights.
 //
 // G threads hold a row, U vectors of V elements each: thread t has the vectors
-// t, t + G, t + 2G, ...  What bounds these kernels beside DRAM is the issue of
+// t, t + G, t + 2G, ...  (Up to 32 threads a row is summed by shuffles, beyond
+// through shared memory, under a barrier of its own.)  What bounds these kernels beside DRAM is the issue of
 // instructions, and every thread of a row pays the row's sums, its root and its
-// addresses; so a thread has 32 elements where the row gives it as many, and the
-// arithmetic is in pairs (two f32 operations an instruction).  It holds the
-// weights of its columns in registers from row to row.
+// addresses; so a thread has many elements, and the arithmetic is in pairs (two
+// f32 operations an instruction).  It holds the weights of its columns in
+// registers from row to row.
 //
 // The CTAs walk over rows of their own.  A thread copies its vectors of coming
 // rows into shared memory that it alone reads (16-byte asynchronous copies: no
@@ -27,15 +28,15 @@
 
 namespace dsix {
 
-constexpr int kNarrowThreads = 128;  // a CTA of rows that lie within a warp
 constexpr int kMaxCols = 32768;
-constexpr int kSms = 152;            // the grids' unit: whole multiples fill a GB300
+constexpr int kSms = 152;  // the grids' unit: whole multiples fill a GB300
 
-template <int G>
+// a CTA of at least `least` threads: one row, or several at a time
+template <int G, int least>
 struct RowShape {
-    static constexpr bool narrow = G <= 32;
-    static constexpr int threads = narrow ? kNarrowThreads : G;
-    static constexpr int rows = narrow ? kNarrowThreads / G : 1;  // of a CTA at a time
+    static constexpr int threads = G > least ? G : least;
+    static constexpr int rows = threads / G;
+    static_assert(G <= 32 || rows <= 15, "a barrier for each row");
 };
 
 // CTAs of so many threads, registers a thread and bytes of shared memory that an SM holds
@@ -48,9 +49,10 @@ constexpr int ctas_per_sm(int threads, int regs, int smem) {
 }
 
 // sums of N numbers over the G threads of a row; s: N * 32 floats of shared
-// memory that no earlier, still unread sum uses (G > 32 only)
+// memory of the CTA that no earlier, still unread sum uses, and `group` the row's
+// place among the CTA's rows (G > 32 only)
 template <int G, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[32]) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[32], int group) {
     constexpr int W = G < 32 ? G : 32;
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1)
@@ -62,9 +64,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[32]) {
         if (lane == 0)
 #pragma unroll
             for (int k = 0; k < N; ++k) s[k][threadIdx.x >> 5] = v[k];
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(G) : "memory");
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = s[k][lane & (warps - 1)];
+        for (int k = 0; k < N; ++k) v[k] = s[k][group * warps + (lane & (warps - 1))];
 #pragma unroll
         for (int o = warps / 2; o > 0; o >>= 1)
 #pragma unroll

@@ -2,7 +2,7 @@
 //
 // One pass over dy and x gives dx and the column sums: a thread holds the same
 // columns of every row it takes, so it adds up their dy * xhat and dy in
-// registers.  The CTAs that walk the rows write their sums once, and a second
+// registers.  The CTAs that walk the rows write their sums once each, and a second
 // kernel adds those in the order of the CTAs (the bits do not depend on which CTA
 // ends first).  Rows too wide for a thread's registers to hold the sums beside
 // the row take their column sums in a pass of their own.
@@ -21,32 +21,32 @@ struct BwdArgs {
     float inv_cols;
 };
 
-// CTAs that write column sums, at most: what their sums cost is bounded, also
-// where the columns are many
-constexpr int max_parts(int cols) { return kSms * (cols <= 512 ? 8 : cols <= 2048 ? 4 : 2); }
+// CTAs that write column sums, at most: one on each SM
+constexpr int kParts = kSms;
 
-// the column sums of the row groups of a CTA: 32 elements of each thread
-constexpr int kGroupSmem = kNarrowThreads * 32 * sizeof(float);
-
+// A CTA of 512 threads has several rows at a time, each under a barrier of its
+// own, so that one CTA fills an SM and leaves one set of column sums: a CTA of a
+// single row leaves 2 to 8 sets an SM, or has too few warps.
 template <class T, int V, int G, int U>
-struct Bwd : RowShape<G> {
+struct Bwd : RowShape<G, 512> {
+    using Shape = RowShape<G, 512>;
     static constexpr int E = U * V, bytes = V * sizeof(T);
-    static constexpr bool hold = G <= 256;  // gamma stays in registers
+    static constexpr bool hold = G < 1024;  // gamma stays in registers
     static constexpr int slots = 2 * U;     // of a thread and stage: x, then dy
-    static constexpr int row = RowShape<G>::threads * slots * bytes;
+    static constexpr int row = Shape::threads * slots * bytes;
     // rows in shared memory: the present one, which both passes over it read
-    // there, and the next one on its way (one row where two would not fit; none
-    // where one would not: both passes then read global memory)
-    static constexpr int stages = kRowSmem / row < 2 ? kRowSmem / row : 2;
+    // there, and the next ones on their way (none where one would not fit: both
+    // passes then read global memory)
+    static constexpr int stages = kRowSmem / row < 4 ? kRowSmem / row : 4;
     static constexpr bool async = bytes >= 4 && stages > 0;
+    // the CTA's column sums of one weight, row by row, take the rows' place in the end
+    static constexpr int cols = G * E, sums_smem = Shape::rows * cols * static_cast<int>(sizeof(float));
     static constexpr int rows_smem = async ? stages * row : 0;
-    static constexpr int smem = RowShape<G>::narrow && rows_smem < kGroupSmem ? kGroupSmem : rows_smem;
-    // the same shape with and without the column sums
-    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, 2 * E + (hold ? E : 0) + 56, smem);
+    static constexpr int smem = rows_smem < sums_smem ? sums_smem : rows_smem;
 };
 
 template <class T, int V, int G, int U, bool kSums, bool kShift>
-__global__ void __launch_bounds__(Bwd<T, V, G, U>::threads, Bwd<T, V, G, U>::ctas) norm_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(const BwdArgs a) {
     using F = Bwd<T, V, G, U>;
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ float s_sum[2][2][32];
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads, Bwd<T, V, G, U>::cta
             shx.template add_products<V>(u, h, x);
         }
         float sums[2] = {sh.total(), shx.total()};
-        row_sums<G>(sums, s_sum[flip]);
+        row_sums<G>(sums, s_sum[flip], sub);
         if (live) {
             const float mh = __fmul_rn(sums[0], a.inv_cols), mhx = __fmul_rn(sums[1], a.inv_cols);
             T* out = static_cast<T*>(a.dx) + row * a.dx_stride;
@@ -202,42 +202,35 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads, Bwd<T, V, G, U>::cta
         rstd = rstd_next;
     }
     if constexpr (kSums) {
+        // the rows' threads, whose columns may lie apart by their shifts, put their
+        // sums into shared memory, where they are added in the rows' order
         float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-        if constexpr (!F::narrow) {
+        float* s_part = reinterpret_cast<float*>(s_rows);
+        if constexpr (F::async) copy_wait<0>();
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int w = 0; w < 2; ++w) {
+            __syncthreads();
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int c = c0 + u * G * V + i;
-                    if (c >= 0 && c < a.cols) {
-                        part[c] = ag[u * V + i];
-                        part[a.cols + c] = ab[u * V + i];
-                    }
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * G * V;
+                const float* v = (w ? ab : ag) + u * V;
+                if constexpr (!kShift && V % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < V; i += 4)
+                        *reinterpret_cast<float4*>(s_part + sub * F::cols + c + i) =
+                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (c + i >= 0) s_part[sub * F::cols + c + i] = v[i];
                 }
-        } else {
-            // the CTA's row groups, whose columns may lie apart by their shifts, meet in
-            // the shared memory of the rows, in the groups' order
-            constexpr int kCols = G * U * V;
-            static_assert(F::rows * kCols * static_cast<int>(sizeof(float)) <= kGroupSmem, "");
-            float* s_part = reinterpret_cast<float*>(s_rows);
-            if constexpr (F::async) copy_wait<0>();
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                __syncthreads();
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int c = c0 + u * G * V + i;
-                        if (c >= 0 && c < a.cols) s_part[sub * kCols + c] = w ? ab[u * V + i] : ag[u * V + i];
-                    }
-                __syncthreads();
-                for (int c = threadIdx.x; c < a.cols; c += F::threads) {
-                    float v = 0.f;
-#pragma unroll
-                    for (int k = 0; k < F::rows; ++k) v += s_part[k * kCols + c];
-                    part[w * a.cols + c] = v;
-                }
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.cols; c += F::threads) {
+                float v = 0.f;
+#pragma unroll 8
+                for (int k = 0; k < F::Shape::rows; ++k) v += s_part[k * F::cols + c];
+                part[w * a.cols + c] = v;
             }
         }
     }
@@ -293,8 +286,7 @@ int launch(const BwdArgs& a, int* parts, cudaStream_t s) {
     static_assert(!kShift || F::async, "the first vector is cut in shared memory");
     int64_t want = (a.rows + F::rows - 1) / F::rows;
     if (kShift) want = (want + V - 1) / V * V;  // CTAs without a row write zero sums
-    const int cap = max_parts(a.cols), most = kSms * F::ctas < cap ? kSms * F::ctas : cap;  // multiples of V
-    const int grid = static_cast<int>(want < most ? want : most);
+    const int grid = static_cast<int>(want < kParts ? want : kParts);  // kParts: a multiple of V
     if (kSums) *parts = grid;
     if constexpr (F::smem > kPlainSmem) {
         const int rc = allow_smem<norm_bwd_kernel<T, V, G, U, kSums, kShift>>(F::smem);
@@ -306,22 +298,20 @@ int launch(const BwdArgs& a, int* parts, cudaStream_t s) {
 
 constexpr int kFusedCols = 16384, kFusedScattered = 8192;  // with column sums
 
-// 32 elements a thread, fewer where the row is short
+// 16 elements a thread: their sums, twice, and gamma leave registers for the rest
 template <class T, bool kSums, bool kShift>
 int by_width(const BwdArgs& a, int* parts, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T), U = 32 / W;
+    constexpr int W = 16 / sizeof(T), U = 16 / W;
     const int n = a.cols + (kShift ? W - 1 : 0);
-    if (n <= 64) return launch<T, W, 8, U / 4, kSums, kShift>(a, parts, s);
-    if (n <= 128) return launch<T, W, 8, U / 2, kSums, kShift>(a, parts, s);
-    if (n <= 256) return launch<T, W, 8, U, kSums, kShift>(a, parts, s);
-    if (n <= 512) return launch<T, W, 16, U, kSums, kShift>(a, parts, s);
-    if (n <= 1024) return launch<T, W, 32, U, kSums, kShift>(a, parts, s);
-    if (n <= 2048) return launch<T, W, 64, U, kSums, kShift>(a, parts, s);
-    if (n <= 4096) return launch<T, W, 128, U, kSums, kShift>(a, parts, s);
-    if (n <= 8192) return launch<T, W, 256, U, kSums, kShift>(a, parts, s);
-    if (n <= kFusedCols) return launch<T, W, 512, U, kSums, kShift>(a, parts, s);
-    if constexpr (!kSums && !kShift) return launch<T, W, 1024, U, false>(a, parts, s);
-    if constexpr (!kSums && kShift) return launch<T, 1, 1024, 32, false>(a, parts, s);
+    if (n <= 128) return launch<T, W, 8, U, kSums, kShift>(a, parts, s);
+    if (n <= 256) return launch<T, W, 16, U, kSums, kShift>(a, parts, s);
+    if (n <= 512) return launch<T, W, 32, U, kSums, kShift>(a, parts, s);
+    if (n <= 1024) return launch<T, W, 64, U, kSums, kShift>(a, parts, s);
+    if (n <= 2048) return launch<T, W, 128, U, kSums, kShift>(a, parts, s);
+    if (n <= 4096) return launch<T, W, 256, U, kSums, kShift>(a, parts, s);
+    if (n <= 8192) return launch<T, W, 512, U, kSums, kShift>(a, parts, s);
+    if (n <= kFusedCols) return launch<T, W, 1024, U, kSums, kShift>(a, parts, s);
+    if constexpr (!kSums) return launch<T, kShift ? 1 : W, 1024, kShift ? 32 : 2 * U, false>(a, parts, s);
     return IX_ERR_UNSUPPORTED;
 }
 
@@ -351,7 +341,7 @@ int dispatch(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
             rc = fused<T, true>(a, how, &parts, s);
         } else {
             // before dx is written: dx may be dy in place
-            parts = static_cast<int>(a.rows < max_parts(a.cols) ? a.rows : max_parts(a.cols));
+            parts = static_cast<int>(a.rows < kParts ? a.rows : kParts);
             norm_cols_kernel<T><<<dim3((a.cols + kColThreads - 1) / kColThreads, parts), kColThreads, 0, s>>>(a);
             rc = launch_status();
             if (rc == IX_OK) rc = fused<T, false>(a, how, nullptr, s);
@@ -371,7 +361,7 @@ using namespace dsix;
 extern "C" size_t ix_layer_norm_bwd_workspace_size(int64_t rows, int cols) {
     if (rows <= 0 || cols <= 0) return 0;
     // rows of an odd width may take some CTAs more than there are rows
-    const int64_t parts = rows + 8 < max_parts(cols) ? rows + 8 : max_parts(cols);
+    const int64_t parts = rows + 8 < kParts ? rows + 8 : kParts;
     return static_cast<size_t>(parts) * 2 * static_cast<size_t>(cols) * sizeof(float);
 }
 

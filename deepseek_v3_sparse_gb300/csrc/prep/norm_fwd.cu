@@ -19,15 +19,16 @@ struct NormArgs {
 };
 
 template <class T, int V, int G, int U>
-struct Fwd : RowShape<G> {
-    static constexpr int E = U * V, bytes = V * sizeof(T), row = RowShape<G>::threads * U * bytes;
+struct Fwd : RowShape<G, 128> {
+    using Shape = RowShape<G, 128>;
+    static constexpr int E = U * V, bytes = V * sizeof(T), row = Shape::threads * U * bytes;
     // the weights stay in registers, as long as the threads of the widest rows have them
     static constexpr bool hold = G < 1024;
     // rows in shared memory: the present one and the next ones on their way
     static constexpr int stages = kRowSmem / row < 3 ? kRowSmem / row : 3;
     static constexpr bool async = bytes >= 4 && stages > 0;
     static constexpr int smem = async ? stages * row : 0;
-    static constexpr int ctas = ctas_per_sm(RowShape<G>::threads, (hold ? 2 * E : 0) + 56, smem);
+    static constexpr int ctas = ctas_per_sm(Shape::threads, (hold ? 2 * E : 0) + 56, smem);
 };
 
 template <class T, int V, int G, int U, bool kShift>
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::cta
             sum.template add<V>(u, f);
         }
         float total[1] = {sum.total()};
-        row_sums<G>(total, s_sum[2 * flip]);
+        row_sums<G>(total, s_sum[2 * flip], sub);
         const float mean = total[0] * a.inv_cols;
         sum.clear();
 #pragma unroll
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::cta
             }
         }
         float sq[1] = {sum.total()};
-        row_sums<G>(sq, s_sum[2 * flip + 1]);
+        row_sums<G>(sq, s_sum[2 * flip + 1], sub);
         const float rstd = rsqrtf(fmaf(sq[0], a.inv_cols, a.eps));
         if (live) {
             if (t == 0 && a.mean) {
