@@ -31,12 +31,13 @@ template <class T, int V, int G, int U>
 struct Bwd : RowShape<G, 512> {
     using Shape = RowShape<G, 512>;
     static constexpr int E = U * V, bytes = V * sizeof(T);
-    static constexpr bool hold = G < 1024;  // gamma stays in registers
+    // gamma stays in registers from row to row, and h and xhat from the row's sums to
+    // its dx, as long as the threads of the widest rows have them
+    static constexpr bool hold = G < 1024;
     static constexpr int slots = 2 * U;     // of a thread and stage: x, then dy
     static constexpr int row = Shape::threads * slots * bytes;
-    // rows in shared memory: the present one, which both passes over it read
-    // there, and the next ones on their way (none where one would not fit: both
-    // passes then read global memory)
+    // rows in shared memory: the present one and the next ones on their way (none
+    // where one would not fit)
     static constexpr int stages = kRowSmem / row < 4 ? kRowSmem / row : 4;
     static constexpr bool async = bytes >= 4 && stages > 0;
     // the CTA's column sums of one weight, row by row, take the rows' place in the end
@@ -50,31 +51,40 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
     using F = Bwd<T, V, G, U>;
     extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ float s_sum[2][2][32];
+    // the rows' mean and rstd, which travel with them, once for each warp (or row within a warp)
+    constexpr int W = G < 32 ? G : 32;
+    __shared__ float s_stat[F::async ? F::stages : 1][F::threads / W][2];
     const int t = threadIdx.x % G, sub = threadIdx.x / G;
     const int64_t step = static_cast<int64_t>(gridDim.x) * F::rows;
     int64_t r0 = static_cast<int64_t>(blockIdx.x) * F::rows;
     const int shift = kShift ? static_cast<int>((r0 + sub) * a.x_stride % V) : 0;
     const int c0 = t * V - shift;  // vector u begins with column c0 + u * G * V
     Vec<T, V>* slot = reinterpret_cast<Vec<T, V>*>(s_rows) + threadIdx.x;  // this thread's, F::threads apart
+    uint32_t bytes[U];  // of vector u that the row has
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * G * V;
+        bytes[u] = c >= a.cols ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
+    }
     auto fetch = [&](int64_t row, int stage) {
-        const T* px = static_cast<const T*>(a.x) + row * a.x_stride;
-        const T* pd = static_cast<const T*>(a.dy) + row * a.dy_stride;
+        const bool live = row < a.rows;
+        const T* px = static_cast<const T*>(a.x) + (live ? row * a.x_stride + c0 : 0);
+        const T* pd = static_cast<const T*>(a.dy) + (live ? row * a.dy_stride + c0 : 0);
         Vec<T, V>* to = slot + stage * F::slots * F::threads;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * G * V;
-            const bool live = row < a.rows && c < a.cols;
-            const uint32_t n = !live ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
-            copy_async<F::bytes>(to + u * F::threads, live ? px + c : a.x, n);
-            copy_async<F::bytes>(to + (U + u) * F::threads, live ? pd + c : a.dy, n);
+        for (int u = 0; u < U; ++u) {  // without bytes to read, the address is not used
+            copy_async<F::bytes>(to + u * F::threads, px + u * G * V, live ? bytes[u] : 0);
+            copy_async<F::bytes>(to + (U + u) * F::threads, pd + u * G * V, live ? bytes[u] : 0);
+        }
+        if (t % W == 0) {
+            copy_async<4>(&s_stat[stage][threadIdx.x / W][0], a.mean + (live ? row : 0), live ? 4 : 0);
+            copy_async<4>(&s_stat[stage][threadIdx.x / W][1], a.rstd + (live ? row : 0), live ? 4 : 0);
         }
         copy_commit();
     };
-    auto stat = [&](const float* p, int64_t row) { return row < a.rows ? __ldg(p + row) : 0.f; };
     if constexpr (F::async) {
         for (int k = 0; k < F::stages; ++k) fetch(r0 + sub + k * step, k);
     }
-    float mean = stat(a.mean, r0 + sub), rstd = stat(a.rstd, r0 + sub);
     float ag[kSums ? F::E : 1], ab[kSums ? F::E : 1], g[F::hold ? U : 1][V];
     if constexpr (kSums) {
         fill<F::E>(ag, 0.f);
@@ -104,7 +114,16 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
                 (live && c < a.cols ? load_vec<T, V>(pd + c) : zero_vec<T, V>()).unpack(d);
             }
         };
-        if constexpr (F::async) copy_wait<F::stages - 1>();
+        float mean, rstd;
+        if constexpr (F::async) {
+            copy_wait<F::stages - 1>();
+            __syncwarp();
+            mean = s_stat[stage][threadIdx.x / W][0];
+            rstd = s_stat[stage][threadIdx.x / W][1];
+        } else {
+            mean = live ? __ldg(a.mean + row) : 0.f;
+            rstd = live ? __ldg(a.rstd + row) : 0.f;
+        }
         if (kShift && t == 0) {  // what lies before the row
 #pragma unroll
             for (int i = 0; i < V - 1; ++i) {
@@ -114,18 +133,20 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
                 }
             }
         }
-        const float mean_next = stat(a.mean, row + step), rstd_next = stat(a.rstd, row + step);
         Pairs<F::E> sh, shx;  // of h and h * xhat
         sh.clear();
         shx.clear();
         const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
         constexpr int keep = F::hold;
+        float xs[F::hold ? U : 1][V], hs[F::hold ? U : 1][V];  // xhat and h
         // (without a test of the column: outside of the row dy = 0)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (!F::hold) weight(0, c0 + u * G * V);
             const float(&w)[V] = g[u * keep];
-            float x[V], d[V], h[V];
+            float(&x)[V] = xs[u * keep];
+            float(&h)[V] = hs[u * keep];
+            float d[V];
             read(u, x, d);
             if constexpr (V % 2 == 0) {
 #pragma unroll
@@ -167,26 +188,30 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + u * G * V;
-                if constexpr (!F::hold) weight(0, c);
-                const float(&w)[V] = g[u * keep];
-                float x[V], d[V];
-                read(u, x, d);
+                float(&x)[V] = xs[u * keep];
+                float(&h)[V] = hs[u * keep];
+                float d[V];
+                if constexpr (!F::hold) {
+                    weight(0, c);
+                    read(u, x, d);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        x[i] = __fmul_rn(__fsub_rn(x[i], mean), rstd);
+                        h[i] = __fmul_rn(d[i], g[0][i]);
+                    }
+                }
                 // dx = rstd * ((h - mh) - xhat * mhx)
                 if constexpr (V % 2 == 0) {
 #pragma unroll
                     for (int i = 0; i < V; i += 2) {
-                        const float2 xh = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), m2), r2);
-                        const float2 h2 = __fmul2_rn(make_float2(d[i], d[i + 1]), make_float2(w[i], w[i + 1]));
-                        float2 y = __fadd2_rn(h2, make_float2(-mh, -mh));
-                        y = __ffma2_rn(xh, make_float2(-mhx, -mhx), y);
+                        float2 y = __fadd2_rn(make_float2(h[i], h[i + 1]), make_float2(-mh, -mh));
+                        y = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(-mhx, -mhx), y);
                         y = __fmul2_rn(y, r2);
                         d[i] = y.x;
                         d[i + 1] = y.y;
                     }
                 } else {
-                    const float xh = __fmul_rn(__fsub_rn(x[0], mean), rstd);
-                    const float h = __fmul_rn(d[0], w[0]);
-                    d[0] = __fmul_rn(rstd, fmaf(-xh, mhx, __fsub_rn(h, mh)));
+                    d[0] = __fmul_rn(rstd, fmaf(-x[0], mhx, __fsub_rn(h[0], mh)));
                 }
                 Vec<T, V> y;
                 y.pack(d);
@@ -198,8 +223,6 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
             stage = stage + 1 == F::stages ? 0 : stage + 1;
         }
         flip ^= 1;
-        mean = mean_next;
-        rstd = rstd_next;
     }
     if constexpr (kSums) {
         // the rows' threads, whose columns may lie apart by their shifts, put their

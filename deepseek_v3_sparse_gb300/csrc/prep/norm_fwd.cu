@@ -42,16 +42,19 @@ __global__ void __launch_bounds__(Fwd<T, V, G, U>::threads, Fwd<T, V, G, U>::cta
     const int shift = kShift ? static_cast<int>((r0 + sub) * a.x_stride % V) : 0;
     const int c0 = t * V - shift;  // vector u begins with column c0 + u * G * V
     Vec<T, V>* slot = reinterpret_cast<Vec<T, V>*>(s_row) + threadIdx.x;  // this thread's, F::threads apart
+    uint32_t bytes[U];  // of vector u that the row has
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * G * V;
+        bytes[u] = c >= a.cols ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
+    }
     auto fetch = [&](int64_t row, int stage) {
-        const T* in = static_cast<const T*>(a.x) + row * a.x_stride;
+        const bool live = row < a.rows;
+        const T* in = static_cast<const T*>(a.x) + (live ? row * a.x_stride + c0 : 0);
         Vec<T, V>* to = slot + stage * U * F::threads;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * G * V;
-            const bool live = row < a.rows && c < a.cols;
-            const uint32_t n = !live ? 0 : kShift ? min(V, a.cols - c) * sizeof(T) : F::bytes;
-            copy_async<F::bytes>(to + u * F::threads, live ? in + c : a.x, n);
-        }
+        for (int u = 0; u < U; ++u)  // without bytes to read, the address is not used
+            copy_async<F::bytes>(to + u * F::threads, in + u * G * V, live ? bytes[u] : 0);
         copy_commit();
     };
     if constexpr (F::async) {
