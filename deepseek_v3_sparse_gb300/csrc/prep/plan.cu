@@ -63,66 +63,74 @@ __device__ __forceinline__ Sums shfl_up(const Sums& s, int d) {
 
 // The exclusive sums of all requests into cn, cc, cb (batch + 1 entries each;
 // shared or global); all threads of the CTA.  `write`: also context_lens, and
-// the status bits.
+// the status bits.  Warps without requests only meet the barriers.
 __device__ void scan_requests(const PlanArgs& a, int32_t* cn, int32_t* cc, int32_t* cb, bool write) {
     __shared__ Sums s_warp[kThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pass = blockDim.x * kItems;
     Sums carry{0, 0, 0};
     bool bad = false;
-    for (int base = 0; base < a.batch; base += kThreads * kItems) {
+#pragma unroll 1
+    for (int base = 0; base < a.batch; base += pass) {
         const int b0 = base + threadIdx.x * kItems;
-        Sums item[kItems], sum{0, 0, 0};
+        const int warps = min(static_cast<int>(blockDim.x) / 32, (a.batch - base + 32 * kItems - 1) / (32 * kItems));
+        Sums item[kItems], ex{0, 0, 0};
+        if (warp < warps) {
+            int c[kItems], n[kItems];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int b = b0 + i;
-            int c = 0, n = 0;
-            if (b < a.batch) {
-                c = __ldg(a.cached + b);
-                n = __ldg(a.fresh + b);
+            for (int i = 0; i < kItems; ++i) {
+                const bool live = b0 + i < a.batch;
+                c[i] = live ? __ldg(a.cached + b0 + i) : 0;
+                n[i] = live ? __ldg(a.fresh + b0 + i) : 0;
             }
-            bad |= c < 0 || n < 0;
-            const uint32_t uc = max(c, 0), un = max(n, 0), all = add_sat(uc, un);
-            bad |= uc + un > kMax;
-            if (write && b < a.batch) a.context_lens[b] = static_cast<int32_t>(all);
-            item[i] = {un, all, blocks_of(a, all) - blocks_of(a, uc)};
-        }
+            Sums sum{0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) sum = sum + item[i];
-        Sums inc = sum;
+            for (int i = 0; i < kItems; ++i) {
+                bad |= c[i] < 0 || n[i] < 0;
+                const uint32_t uc = max(c[i], 0), un = max(n[i], 0), all = add_sat(uc, un);
+                bad |= uc + un > kMax;
+                if (write && b0 + i < a.batch) a.context_lens[b0 + i] = static_cast<int32_t>(all);
+                item[i] = {un, all, blocks_of(a, all) - blocks_of(a, uc)};
+                sum = sum + item[i];
+            }
+            Sums inc = sum;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const Sums o = shfl_up(inc, d);
-            if (lane >= d) inc = inc + o;
+            for (int d = 1; d < 32; d <<= 1) {
+                const Sums o = shfl_up(inc, d);
+                if (lane >= d) inc = inc + o;
+            }
+            if (lane == 31) s_warp[warp] = inc;
+            ex = shfl_up(inc, 1);
+            if (lane == 0) ex = {0, 0, 0};
         }
-        if (lane == 31) s_warp[warp] = inc;
         __syncthreads();
-        Sums total{0, 0, 0}, before{0, 0, 0};
+        if (warp < warps) {
+            ex = carry + ex;
+#pragma unroll 1
+            for (int w = 0; w < warp; ++w) ex = ex + s_warp[w];
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w == warp) before = total;
-            total = total + s_warp[w];
-        }
-        Sums ex = shfl_up(inc, 1);
-        if (lane == 0) ex = {0, 0, 0};
-        ex = carry + before + ex;
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            if (b0 + i < a.batch) {
-                cn[b0 + i] = static_cast<int32_t>(ex.n);
-                cc[b0 + i] = static_cast<int32_t>(ex.c);
-                cb[b0 + i] = static_cast<int32_t>(ex.b);
+            for (int i = 0; i < kItems; ++i) {
+                if (b0 + i < a.batch) {
+                    cn[b0 + i] = static_cast<int32_t>(ex.n);
+                    cc[b0 + i] = static_cast<int32_t>(ex.c);
+                    cb[b0 + i] = static_cast<int32_t>(ex.b);
+                }
+                ex = ex + item[i];
+                if (b0 + i == a.batch - 1) {
+                    cn[a.batch] = static_cast<int32_t>(ex.n);
+                    cc[a.batch] = static_cast<int32_t>(ex.c);
+                    cb[a.batch] = static_cast<int32_t>(ex.b);
+                    bad |= ex.n == kMax || ex.c == kMax || ex.b == kMax;
+                }
             }
-            ex = ex + item[i];
         }
-        carry = carry + total;
-        __syncthreads();  // s_warp is written again
+        if (base + pass < a.batch) {
+#pragma unroll 1
+            for (int w = 0; w < warps; ++w) carry = carry + s_warp[w];
+            __syncthreads();  // s_warp is written again
+        }
     }
-    if (threadIdx.x == 0) {
-        cn[a.batch] = static_cast<int32_t>(carry.n);
-        cc[a.batch] = static_cast<int32_t>(carry.c);
-        cb[a.batch] = static_cast<int32_t>(carry.b);
-        bad |= carry.n == kMax || carry.c == kMax || carry.b == kMax;
-    }
+    if (a.batch == 0 && threadIdx.x == 0) cn[0] = cc[0] = cb[0] = 0;
     if (write && bad) flag(a.status, IX_DEV_BAD_RANGE);
 }
 
@@ -291,7 +299,7 @@ extern "C" int ix_plan_step(const int32_t* cached_lens, const int32_t* new_lens,
                      bt_stride, bt_width, context_lens, cu_new, cu_ctx, cu_blocks, slot_mapping, positions,
                      row_req, row_len, ks, ke, rows, st};
     const int64_t want = (rows + kThreads * kRows - 1) / (kThreads * kRows);
-    const int grid = static_cast<int>(want < 1 ? 1 : want > 4 * sms ? 4 * sms : want);
+    const int grid = static_cast<int>(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (batch <= kFusedBatch) {
         const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);
