@@ -1,11 +1,11 @@
-"""Build libdsix.so (the CUDA library behind include/dsix.h) and libdsix_prep.so
-(include/dsix_prep.h) in-tree.
+"""Build libdsix.so (the CUDA library behind include/dsix.h), libdsix_prep.so
+(include/dsix_prep.h) and _prep.so (its Python binding) in-tree.
 
 Every translation unit under csrc/ (libdsix) and csrc/prep/ (libdsix_prep) is
 compiled for sm_103a only (``-gencode arch=compute_103a,code=sm_103a``), in
 parallel, then linked into ``deepseek_v3_sparse_gb300/`` with the CUDA runtime
-linked statically.  No cmake; a rebuild is skipped when a library is newer than
-every source.
+linked statically.  The binding is host C++ against torch's headers.  No cmake; a
+rebuild is skipped when a library is newer than every source.
 """
 from __future__ import annotations
 
@@ -14,12 +14,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdsix.so")
 OUT_PREP = os.path.join(HERE, "libdsix_prep.so")
+OUT_BINDING = os.path.join(HERE, "_prep.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,10 +57,31 @@ def up_to_date(out: str = OUT) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps(out))
 
 
+def _binding_flags():
+    """Compiler and linker arguments of the binding: torch's headers and libraries."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include"), os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    compile_args = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"]
+    for d in include:
+        compile_args += ["-isystem", d]
+    link = ["-shared", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L" + HERE, "-l:libdsix_prep.so", "-Wl,-rpath,$ORIGIN"]
+    return compile_args, link
+
+
+def _binding_up_to_date() -> bool:
+    src = os.path.join(CSRC, "prep", "binding.cpp")
+    deps = [src, os.path.join(ROOT, "include", "dsix_prep.h"), os.path.join(ROOT, "include", "dsix.h"), __file__]
+    return os.path.exists(OUT_BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(OUT_BINDING) for p in deps)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Builds what is out of date; returns libdsix.so's path."""
     todo = [out for out in LIBRARIES if force or not up_to_date(out)]
-    if not todo:
+    binding = force or not _binding_up_to_date()
+    if not todo and not binding:
         return OUT
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -76,15 +99,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        objs = {out: [ex.submit(compile_one, src) for src in _sources(out)] for out in todo}
-    for out in todo:
-        tmp = out + f".tmp{os.getpid()}"
-        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o.result() for o in objs[out]], "-cudart", "static"]
+    def compile_binding(obj):
+        cmd = [os.environ.get("CXX", "g++"), *_binding_flags()[0], "-c", os.path.join(CSRC, "prep", "binding.cpp"),
+               "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stderr}")
+        return obj
+
+    def link(cmd, out):
+        tmp = out + f".tmp{os.getpid()}"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, out)
+
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        host = ex.submit(compile_binding, os.path.join(BUILD_DIR, "prep_binding.cpp.o")) if binding else None
+        objs = {out: [ex.submit(compile_one, src) for src in _sources(out)] for out in todo}
+    for out in todo:
+        link([nvcc, *ARCH, "-shared", *[o.result() for o in objs[out]], "-cudart", "static"], out)
+    if host is not None:
+        link([os.environ.get("CXX", "g++"), host.result(), *_binding_flags()[1]], OUT_BINDING)
     return OUT
 
 

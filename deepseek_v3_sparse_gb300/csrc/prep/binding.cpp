@@ -1,0 +1,389 @@
+// binding.cpp -- the Python binding of libdsix_prep's stream calls.
+//
+// A step's small calls cost more on the host than on the GPU, and most of that
+// is looking at tensors, so the checks and the marshalling are here and not in
+// Python (a call of fourteen tensors: 11.6 us there, see prep.py).  Each function
+// takes its tensors in the order of the package's function of the same name, then
+// its numbers, then the stream's handle or None (torch's current stream).  It
+// checks shapes first, then that every tensor lies on the current device, and
+// returns the library's status; what the checks refuse is raised as the error
+// class that set_error was given, or as a TypeError.
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <sstream>
+#include <string>
+#include <vector>
+
+#include "../../../include/dsix_prep.h"
+
+namespace {
+
+PyObject* g_error = nullptr;  // the package's DsixError
+
+struct Refused {
+    PyObject* type;
+    std::string what;
+};
+struct Raised {};  // a Python error is set
+
+[[noreturn]] void refuse(const std::string& what) { throw Refused{g_error ? g_error : PyExc_RuntimeError, what}; }
+
+std::string text(at::IntArrayRef s) {
+    std::ostringstream o;
+    o << "(";
+    for (size_t i = 0; i < s.size(); ++i) o << (i ? ", " : "") << s[i];
+    o << (s.size() == 1 ? ",)" : ")");
+    return o.str();
+}
+
+std::string text(at::ScalarType t) { return std::string("torch.") + c10::toString(t); }
+
+const at::Tensor& tensor(PyObject* o, const char* name, int dim = -1) {
+    if (!THPVariable_Check(o)) throw Refused{PyExc_TypeError, std::string(name) + ": expected a torch.Tensor"};
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (dim >= 0 && t.dim() != dim)
+        refuse(std::string(name) + ": shape " + text(t.sizes()) + ", expected " + std::to_string(dim) + " dimensions");
+    return t;
+}
+
+// a tensor of at least n elements
+const at::Tensor& flat(PyObject* o, int64_t n, const char* name) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.numel() < n)
+        refuse(std::string(name) + ": " + std::to_string(t.numel()) + " elements, expected >= " + std::to_string(n));
+    return t;
+}
+
+int dtype_of(const at::Tensor& t, const char* name) {
+    switch (t.scalar_type()) {
+        case at::kBFloat16: return IX_BF16;
+        case at::kHalf: return IX_FP16;
+        case at::kFloat: return IX_FP32;
+        default:
+            throw Refused{PyExc_TypeError,
+                          std::string(name) + ": dtype " + text(t.scalar_type()) + ", expected bf16, fp16 or f32"};
+    }
+}
+
+void of_type(const at::Tensor& t, at::ScalarType type, const char* name) {
+    if (t.scalar_type() != type)
+        throw Refused{PyExc_TypeError,
+                      std::string(name) + ": dtype " + text(t.scalar_type()) + ", expected " + text(type)};
+}
+
+// an activation of the shape given, its last dimension contiguous
+const at::Tensor& strided(PyObject* o, const char* name, at::IntArrayRef shape) {
+    const at::Tensor& t = tensor(o, name, static_cast<int>(shape.size()));
+    if (t.sizes() != shape) refuse(std::string(name) + ": shape " + text(t.sizes()) + ", expected " + text(shape));
+    if (shape.back() > 1 && t.stride(-1) != 1) refuse(std::string(name) + ": the last dimension must be contiguous");
+    return t;
+}
+
+// the current device, on which every tensor of a call has to be: the library launches there
+struct Device {
+    int index;
+    explicit Device(const at::Tensor& t, const char* name) : index(-1) {
+        if (!t.is_cuda()) refuse(std::string(name) + ": must be a CUDA tensor");
+        index = c10::cuda::current_device();
+        check(t, name);
+    }
+    void check(const at::Tensor& t, const char* name) const {
+        if (!t.is_cuda()) refuse(std::string(name) + ": must be a CUDA tensor");
+        if (t.get_device() != index)
+            refuse(std::string(name) + ": on " + t.device().str() + ", but the current device is cuda:" +
+                   std::to_string(index));
+    }
+    // the address of an activation
+    void* strided(const at::Tensor& t, const char* name) const {
+        check(t, name);
+        return t.data_ptr();
+    }
+    // the address of a contiguous tensor of a type
+    template <class P>
+    P* plain(const at::Tensor& t, at::ScalarType type, const char* name) const {
+        check(t, name);
+        of_type(t, type, name);
+        if (!t.is_contiguous()) refuse(std::string(name) + ": must be contiguous");
+        return static_cast<P*>(t.data_ptr());
+    }
+    ix_stream_t stream(PyObject* handle) const {
+        if (handle == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
+        void* p = PyLong_AsVoidPtr(handle);
+        if (PyErr_Occurred()) throw Raised{};
+        return static_cast<ix_stream_t>(p);
+    }
+};
+
+int64_t integer(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+
+int small(PyObject* o, const char* name) {
+    const int64_t v = integer(o);
+    if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(name) + ": out of range");
+    return static_cast<int>(v);
+}
+
+int small(int64_t v, const char* name) {
+    if (v > INT32_MAX) refuse(std::string(name) + ": too many");
+    return static_cast<int>(v);
+}
+
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
+
+// Runs a call's body; nothing but a Python error leaves it.
+template <class F>
+PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F body) {
+    if (got != want) {
+        PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
+        return nullptr;
+    }
+    try {
+        return PyLong_FromLong(body());
+    } catch (const Refused& r) {
+        PyErr_SetString(r.type, r.what.c_str());
+    } catch (const Raised&) {
+    } catch (const std::exception& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    }
+    return nullptr;
+}
+
+PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 16, [&] {
+        const at::Tensor& cached = tensor(a[0], "cached_lens", 1);
+        const int64_t batch = cached.size(0);
+        const at::Tensor& fresh = flat(a[1], batch, "new_lens");
+        const at::Tensor& free = tensor(a[2], "free_blocks", 1);
+        const at::Tensor& table = tensor(a[3], "block_table", 2);
+        if (table.size(0) < batch)
+            refuse("block_table: " + std::to_string(table.size(0)) + " rows, expected >= " + std::to_string(batch));
+        const at::Tensor& ctx = flat(a[4], batch, "context_lens");
+        const at::Tensor& cu_new = flat(a[5], batch + 1, "cu_new");
+        const at::Tensor& cu_ctx = flat(a[6], batch + 1, "cu_ctx");
+        const at::Tensor& cu_blocks = flat(a[7], batch + 1, "cu_blocks");
+        const at::Tensor& slots = tensor(a[8], "slot_mapping", 1);
+        const int64_t rows = slots.size(0);
+        const at::Tensor& positions = flat(a[9], rows, "positions");
+        const at::Tensor& row_req = flat(a[10], rows, "row_req");
+        const at::Tensor& row_len = flat(a[11], rows, "row_len");
+        const at::Tensor& ks = flat(a[12], rows, "ks");
+        const at::Tensor& ke = flat(a[13], rows, "ke");
+        const Device dev(cached, "cached_lens");
+        auto i32 = [&](const at::Tensor& t, const char* name) { return dev.plain<int32_t>(t, at::kInt, name); };
+        auto i64 = [&](const at::Tensor& t, const char* name) { return dev.plain<int64_t>(t, at::kLong, name); };
+        return ix_plan_step(i32(cached, "cached_lens"), i32(fresh, "new_lens"), small(batch, "cached_lens"),
+                            small(a[14], "block_size"), i32(free, "free_blocks"), free.size(0),
+                            i32(table, "block_table"), table.size(1), small(table.size(1), "block_table"),
+                            i32(ctx, "context_lens"), i32(cu_new, "cu_new"), i32(cu_ctx, "cu_ctx"),
+                            i32(cu_blocks, "cu_blocks"), i64(slots, "slot_mapping"), i64(positions, "positions"),
+                            i32(row_req, "row_req"), i32(row_len, "row_len"), i32(ks, "ks"), i32(ke, "ke"), rows,
+                            dev.stream(a[15]));
+    });
+}
+
+PyObject* rope_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&] {
+        const at::Tensor& out = tensor(a[0], "cos_sin", 2);
+        PyObject* list = PySequence_Fast(a[1], "inv_freq: expected a sequence of numbers");
+        if (!list) throw Raised{};
+        std::vector<double> freq(static_cast<size_t>(PySequence_Fast_GET_SIZE(list)));
+        for (size_t i = 0; i < freq.size(); ++i)
+            freq[i] = PyFloat_AsDouble(PySequence_Fast_GET_ITEM(list, static_cast<Py_ssize_t>(i)));
+        Py_DECREF(list);
+        if (PyErr_Occurred()) throw Raised{};
+        if (out.size(1) != 2 * static_cast<int64_t>(freq.size()))
+            refuse("inv_freq: " + std::to_string(freq.size()) + " values, cos_sin has " + std::to_string(out.size(1)) +
+                   " columns");
+        const Device dev(out, "cos_sin");
+        return ix_rope_table(freq.data(), small(out.size(1), "cos_sin"), integer(a[2]), out.size(0), number(a[3]),
+                             dev.plain<float>(out, at::kFloat, "cos_sin"), dev.stream(a[4]));
+    });
+}
+
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor& x = tensor(a[0], "x", 3);
+        strided(a[0], "x", x.sizes());
+        const int dtype = dtype_of(x, "x");
+        const at::Tensor& out = strided(a[3], "out", x.sizes());
+        of_type(out, x.scalar_type(), "out");
+        const at::Tensor *x2 = nullptr, *out2 = nullptr;
+        if (a[7] != Py_None) {
+            x2 = &tensor(a[7], "x2", 3);
+            const int64_t shape[3] = {x.size(0), x2->size(1), x.size(2)};
+            strided(a[7], "x2", shape);
+            of_type(*x2, x.scalar_type(), "x2");
+            out2 = &strided(a[8], "out2", shape);
+            of_type(*out2, x.scalar_type(), "out2");
+        }
+        const at::Tensor& positions = flat(a[1], x.size(0), "positions");
+        const at::Tensor& table = tensor(a[2], "cos_sin", 2);
+        const Device dev(x, "x");
+        auto side = [&](const at::Tensor& from, const at::Tensor& to, const char* f, const char* t) {
+            return ix_rope_tensor{dev.strided(from, f), dev.strided(to, t), small(from.size(1), f), from.stride(0),
+                                  from.stride(1), to.stride(0), to.stride(1)};
+        };
+        const ix_rope_tensor one = side(x, out, "x", "out");
+        ix_rope_tensor two;
+        if (x2) two = side(*x2, *out2, "x2", "out2");
+        return ix_rope(&one, x2 ? &two : nullptr, dtype, x.size(0), small(x.size(2), "x"), small(a[4], "offset"),
+                       dev.plain<int64_t>(positions, at::kLong, "positions"),
+                       dev.plain<float>(table, at::kFloat, "cos_sin"), table.size(0), small(table.size(1), "cos_sin"),
+                       (truth(a[5]) ? IX_ROPE_INTERLEAVED : 0) | (truth(a[6]) ? IX_ROPE_INVERSE : 0), dev.stream(a[9]));
+    });
+}
+
+// the weights of a norm: f32 or of the activations' type, all the same; NULL where there is none
+struct Weights {
+    at::ScalarType type = at::kFloat;
+    bool any = false;
+    const at::Tensor* get(PyObject* o, const char* name, int64_t cols, at::ScalarType x) {
+        if (o == Py_None) return nullptr;
+        const at::Tensor& t = tensor(o, name, 1);
+        if (t.size(0) != cols)
+            refuse(std::string(name) + ": " + std::to_string(t.size(0)) + " elements, expected " + std::to_string(cols));
+        if (t.scalar_type() != at::kFloat && t.scalar_type() != x)
+            throw Refused{PyExc_TypeError, std::string(name) + ": dtype " + text(t.scalar_type()) + ", expected " +
+                                               text(at::kFloat) + " or " + text(x)};
+        if (any && t.scalar_type() != type)
+            refuse(std::string(name) + ": dtype " + text(t.scalar_type()) + ", the other weights have " + text(type));
+        any = true;
+        type = t.scalar_type();
+        return &t;
+    }
+    int dtype() const { return type == at::kFloat ? IX_FP32 : type == at::kHalf ? IX_FP16 : IX_BF16; }
+    const void* pointer(const Device& dev, const at::Tensor* t, const char* name) const {
+        return t ? dev.plain<void>(*t, type, name) : nullptr;
+    }
+};
+
+const at::Tensor* optional(PyObject* o, int64_t n, const char* name) {
+    return o == Py_None ? nullptr : &flat(o, n, name);
+}
+
+float* f32(const Device& dev, const at::Tensor* t, const char* name) {
+    return t ? dev.plain<float>(*t, at::kFloat, name) : nullptr;
+}
+
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&] {
+        const at::Tensor& x = tensor(a[0], "x", 2);
+        const int64_t rows = x.size(0), cols = x.size(1);
+        strided(a[0], "x", x.sizes());
+        const int dtype = dtype_of(x, "x");
+        const at::Tensor& out = strided(a[4], "out", x.sizes());
+        of_type(out, x.scalar_type(), "out");
+        Weights w;
+        const at::Tensor* gamma = w.get(a[1], "gamma", cols, x.scalar_type());
+        const at::Tensor* beta = w.get(a[2], "beta", cols, x.scalar_type());
+        const at::Tensor* mean = optional(a[5], rows, "mean");
+        const at::Tensor* rstd = optional(a[6], rows, "rstd");
+        if (!mean != !rstd) refuse("mean and rstd: both or neither");
+        const Device dev(x, "x");
+        return ix_layer_norm(x.data_ptr(), x.stride(0), w.pointer(dev, gamma, "gamma"), w.pointer(dev, beta, "beta"),
+                             w.dtype(), static_cast<float>(number(a[3])), rows, small(cols, "x"),
+                             dev.strided(out, "out"), out.stride(0), f32(dev, mean, "mean"), f32(dev, rstd, "rstd"),
+                             dtype, dev.stream(a[7]));
+    });
+}
+
+PyObject* layer_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&] {
+        const at::Tensor& x = tensor(a[1], "x", 2);
+        const int64_t rows = x.size(0), cols = x.size(1);
+        strided(a[1], "x", x.sizes());
+        const int dtype = dtype_of(x, "x");
+        const at::Tensor& dy = strided(a[0], "dy", x.sizes());
+        of_type(dy, x.scalar_type(), "dy");
+        const at::Tensor& dx = strided(a[5], "dx", x.sizes());
+        of_type(dx, x.scalar_type(), "dx");
+        Weights w;
+        const at::Tensor* gamma = w.get(a[2], "gamma", cols, x.scalar_type());
+        const at::Tensor& mean = flat(a[3], rows, "mean");
+        const at::Tensor& rstd = flat(a[4], rows, "rstd");
+        const at::Tensor* dgamma = optional(a[6], cols, "dgamma");
+        const at::Tensor* dbeta = optional(a[7], cols, "dbeta");
+        if (!dgamma != !dbeta) refuse("dgamma and dbeta: both or neither");
+        const at::Tensor* work = optional(a[8], 0, "workspace");
+        const Device dev(x, "x");
+        return ix_layer_norm_bwd(dev.strided(dy, "dy"), dy.stride(0), x.data_ptr(), x.stride(0),
+                                 w.pointer(dev, gamma, "gamma"), w.dtype(), f32(dev, &mean, "mean"),
+                                 f32(dev, &rstd, "rstd"), rows, small(cols, "x"), dev.strided(dx, "dx"), dx.stride(0),
+                                 f32(dev, dgamma, "dgamma"), f32(dev, dbeta, "dbeta"), dtype,
+                                 work ? dev.plain<void>(*work, at::kByte, "workspace") : nullptr,
+                                 work ? static_cast<size_t>(work->numel()) : 0, dev.stream(a[9]));
+    });
+}
+
+PyObject* norm_rope_write_k(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&] {
+        constexpr int64_t kDim = 128;
+        const at::Tensor& k = tensor(a[0], "k", 2);
+        const int64_t tokens = k.size(0), shape[2] = {tokens, kDim};
+        strided(a[0], "k", shape);
+        const int dtype = dtype_of(k, "k");
+        const at::Tensor& gamma = flat(a[1], kDim, "gamma");
+        const at::Tensor& beta = flat(a[2], kDim, "beta");
+        const at::Tensor& positions = flat(a[4], tokens, "positions");
+        const at::Tensor& table = tensor(a[5], "cos_sin", 2);
+        const at::Tensor& slots = flat(a[6], tokens, "slot_mapping");
+        const at::Tensor& cache = tensor(a[7], "cache", 2);
+        const int block_size = small(a[10], "block_size");
+        if (cache.size(1) != block_size * (kDim + 4))
+            refuse("cache: " + std::to_string(cache.size(1)) + " bytes a block, expected " +
+                   std::to_string(block_size * (kDim + 4)));
+        const Device dev(k, "k");
+        return ix_norm_rope_write_k(
+            k.data_ptr(), k.stride(0), dtype, tokens, f32(dev, &gamma, "gamma"), f32(dev, &beta, "beta"),
+            static_cast<float>(number(a[3])), dev.plain<int64_t>(positions, at::kLong, "positions"),
+            f32(dev, &table, "cos_sin"), table.size(0), small(table.size(1), "cos_sin"), small(a[8], "rope_offset"),
+            truth(a[9]) ? 1 : 0, dev.plain<int64_t>(slots, at::kLong, "slot_mapping"),
+            dev.plain<uint8_t>(cache, at::kByte, "cache"), cache.size(0), block_size, dev.stream(a[11]));
+    });
+}
+
+PyObject* set_error(PyObject*, PyObject* type) {
+    Py_INCREF(type);
+    Py_XDECREF(g_error);
+    g_error = type;
+    Py_RETURN_NONE;
+}
+
+template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyCFunction fast() {
+    return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
+}
+
+PyMethodDef g_methods[] = {
+    {"plan_step", fast<plan_step>(), METH_FASTCALL, nullptr},
+    {"rope_table", fast<rope_table>(), METH_FASTCALL, nullptr},
+    {"rope", fast<rope>(), METH_FASTCALL, nullptr},
+    {"layer_norm", fast<layer_norm>(), METH_FASTCALL, nullptr},
+    {"layer_norm_bwd", fast<layer_norm_bwd>(), METH_FASTCALL, nullptr},
+    {"norm_rope_write_k", fast<norm_rope_write_k>(), METH_FASTCALL, nullptr},
+    {"set_error", set_error, METH_O, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_prep", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__prep() { return PyModule_Create(&g_module); }
