@@ -16,7 +16,7 @@ constexpr int64_t kMaxItems = 1ll << 30;
 // the wrapping product p * F is the angle modulo one turn, exact but for F's
 // rounding.  The nearest quarter turn is split off in integers; what is left, an
 // eighth of a turn at most, goes to radians in f32 with its relative accuracy
-// intact, also next to the zeros, and through the Taylor series of sine and
+// (two roundings) intact, also next to the zeros, and through the Taylor series of sine and
 // cosine: at pi / 4 the first terms left out are x^11 / 11! = 1.8e-9 and
 // x^12 / 12! = 1.2e-10, below a tenth of a rounding.
 //
@@ -27,25 +27,43 @@ struct TurnTable {
     uint64_t step[kMaxPairs];
 };
 
-__device__ __forceinline__ void sincos_turn(uint64_t turn, float amplitude, float& s, float& c) {
-    const uint64_t quarter = (turn + (1ull << 61)) >> 62;
-    const int64_t rest = static_cast<int64_t>(turn - (quarter << 62));
-    const float x = __ll2float_rn(rest) * static_cast<float>(6.283185307179586 * 0x1p-64);
-    const float q = x * x;
-    float ps = fmaf(q, 1.f / 362880, -1.f / 5040);
-    ps = fmaf(q, ps, 1.f / 120);
-    ps = fmaf(q, ps, -1.f / 6);
-    const float sn = fmaf(x * q, ps, x);
-    float pc = fmaf(q, -1.f / 3628800, 1.f / 40320);
-    pc = fmaf(q, pc, -1.f / 720);
-    pc = fmaf(q, pc, 1.f / 24);
-    pc = fmaf(q, pc, -0.5f);
-    const float cs = fmaf(q, pc, 1.f);
-    const uint32_t k = static_cast<uint32_t>(quarter);
-    s = amplitude * (k & 1 ? cs : sn);
-    c = amplitude * (k & 1 ? sn : cs);
-    if (k & 2) s = -s;
-    if ((k + 1) & 2) c = -c;
+// an angle's quarter turns, and the rest of it in radians; the rest's low word
+// counts where its high word is small
+__device__ __forceinline__ float split_turn(uint64_t turn, uint32_t& quarters) {
+    const uint32_t hi = static_cast<uint32_t>(turn >> 32), lo = static_cast<uint32_t>(turn);
+    quarters = (hi + 0x20000000u) >> 30;
+    const int32_t rest = static_cast<int32_t>(hi - (quarters << 30));
+    constexpr double kRadians = 6.283185307179586;
+    return fmaf(static_cast<float>(lo), static_cast<float>(kRadians * 0x1p-64),
+                static_cast<float>(rest) * static_cast<float>(kRadians * 0x1p-32));
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// amplitude * sine and cosine of two angles, in pairs of f32 operations
+__device__ __forceinline__ void sincos_turns(uint64_t t0, uint64_t t1, float amplitude, float2& s, float2& c) {
+    uint32_t k0, k1;
+    float2 x;
+    x.x = split_turn(t0, k0);
+    x.y = split_turn(t1, k1);
+    const float2 q = __fmul2_rn(x, x);
+    float2 ps = __ffma2_rn(q, both(1.f / 362880), both(-1.f / 5040));
+    ps = __ffma2_rn(q, ps, both(1.f / 120));
+    ps = __ffma2_rn(q, ps, both(-1.f / 6));
+    x = __fmul2_rn(x, both(amplitude));
+    const float2 sn = __ffma2_rn(__fmul2_rn(x, q), ps, x);
+    float2 pc = __ffma2_rn(q, both(-1.f / 3628800), both(1.f / 40320));
+    pc = __ffma2_rn(q, pc, both(-1.f / 720));
+    pc = __ffma2_rn(q, pc, both(1.f / 24));
+    pc = __ffma2_rn(q, pc, both(-0.5f));
+    const float2 cs = __ffma2_rn(__fmul2_rn(q, both(amplitude)), pc, both(amplitude));
+    // by the quarter: (s, c), (c, -s), (-s, -c), (-c, s)
+    auto place = [](uint32_t k, float sn, float cs, float& s, float& c) {
+        s = __uint_as_float(__float_as_uint(k & 1 ? cs : sn) ^ ((k & 2) << 30));
+        c = __uint_as_float(__float_as_uint(k & 1 ? sn : cs) ^ (((k + 1) & 2) << 30));
+    };
+    place(k0, sn.x, cs.x, s.x, c.x);
+    place(k1, sn.y, cs.y, s.y, c.y);
 }
 
 template <int W>
@@ -67,10 +85,18 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
     for (; r < n; r += stride) {
         Vec<float, W> s, c;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            sincos_turn(turn[i], amplitude, s.v[i], c.v[i]);
-            turn[i] += step[i];
+        for (int i = 0; i < W; i += 2) {
+            float2 s2, c2;
+            sincos_turns(turn[i], turn[i + 1 < W ? i + 1 : i], amplitude, s2, c2);
+            s.v[i] = s2.x;
+            c.v[i] = c2.x;
+            if (i + 1 < W) {
+                s.v[i + 1] = s2.y;
+                c.v[i + 1] = c2.y;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < W; ++i) turn[i] += step[i];
         float* row = out + r * 2 * pairs + q * W;
         store_vec<float, W>(row, c);
         store_vec<float, W>(row + pairs, s);
