@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
         flip ^= 1;
     }
     if constexpr (kSums) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // the rows' threads, whose columns may lie apart by their shifts, put their
         // sums into shared memory, where they are added in the rows' order
         float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kColThreads) norm_cols_kernel(const BwdArgs a)
 __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int parts, int cols, float* dgamma,
                                                           float* dbeta) {
     __shared__ float s[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the parts are whole only now
     const int i = blockIdx.x * 32 + threadIdx.x;  // column of [dgamma | dbeta]
     float v = 0.f;
     if (i < 2 * cols) {
@@ -372,7 +374,19 @@ int dispatch(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
         if (rc != IX_OK) return rc;
     }
     if (!dgamma) return IX_OK;
-    norm_parts_kernel<<<(2 * a.cols + 31) / 32, dim3(32, 32), 0, s>>>(a.part, parts, a.cols, dgamma, dbeta);
+    // its launch overlaps the first kernel's end
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((2 * a.cols + 31) / 32);
+    config.blockDim = dim3(32, 32);
+    config.stream = s;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    if (cudaLaunchKernelEx(&config, norm_parts_kernel, static_cast<const float*>(a.part), parts, a.cols, dgamma,
+                           dbeta) != cudaSuccess)
+        return IX_ERR_CUDA;
     return launch_status();
 }
 

@@ -166,6 +166,21 @@ def test_sums_saturate(dsix):
     assert t["positions"].tolist() == [big, big] and t["cu_new"].tolist() == [0, 1, 2, 2]
 
 
+@pytest.mark.parametrize("shift", [2, 4])
+def test_buffers_that_start_elsewhere(dsix, shift):
+    """The 64-bit outputs on 16 and on 32 bytes (their stores differ), the others on 16."""
+    g = torch.Generator().manual_seed(shift)
+    new, cached = torch.randint(0, 90, (300,), generator=g).tolist(), torch.randint(0, 200, (300,), generator=g).tolist()
+    t = check(dsix, cached, new)
+    moved = dict(t)
+    for name in ("slot_mapping", "positions", "row_req", "row_len", "ks", "ke"):
+        n = shift if t[name].dtype is torch.int64 else 4
+        moved[name] = torch.full((n + t[name].numel(),), -77, dtype=t[name].dtype, device="cuda")[n:]
+    dsix.ix_plan_step(**moved)
+    assert dsix.ix_prep_device_status() == 0
+    assert all(torch.equal(moved[k], t[k]) for k in t)
+
+
 def test_graph_and_side_stream(dsix):
     t = check(dsix, [10, 640], [3, 70])
     want = {k: v.clone() for k, v in t.items()}
