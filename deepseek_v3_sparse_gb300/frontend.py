@@ -1,0 +1,57 @@
+"""From request lengths and raw projections to what the indexer's calls consume.
+
+A serving step begins with lengths (how many tokens each request has in the
+cache and how many it brings) and the projections of its new tokens.  FrontEnd
+chains the calls that turn them into the inputs of the logits and top-k calls:
+
+  1. ix_plan_step          block table, slots, positions, row ranges
+  2. ix_norm_rope_write_k  the keys: layer norm, rotary positions, fp8, paged cache
+  3. ix_rope               the queries' rotary positions
+  4. ix_quant_q            the queries' fp8 codes, their scales folded into the weights
+
+All buffers are allocated once; ``run`` allocates nothing and never
+synchronises, so it can be captured in a CUDA graph, together with the calls
+that follow it, and replayed with other lengths in the same tensors.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (BLOCK_SIZE, HEAD_DIM, HEADS, ix_norm_rope_write_k, ix_plan_step, ix_quant_q, ix_rope)
+
+
+class FrontEnd:
+    """block_table [B, width] int32 and free_blocks [F] int32 are the server's (the plan fills in the blocks it
+    takes; the caller moves free_blocks on by cu_blocks[-1], which it can count from the lengths); cache is the
+    indexer-K cache; gamma, beta [128] f32 and eps the key norm's; cos_sin [max_pos, rot] the rotary table.
+    ``rows`` is the most new tokens of a step; rows that a step does not use are empty (slot -1, length 0)."""
+
+    def __init__(self, *, rows: int, block_table: torch.Tensor, free_blocks: torch.Tensor, cache: torch.Tensor,
+                 gamma: torch.Tensor, beta: torch.Tensor, eps: float, cos_sin: torch.Tensor, rope_offset: int = 0,
+                 interleaved: bool = False, heads: int = HEADS):
+        dev, batch = block_table.device, block_table.shape[0]
+        i32 = dict(dtype=torch.int32, device=dev)
+        i64 = dict(dtype=torch.int64, device=dev)
+        self.block_table, self.free_blocks, self.cache = block_table, free_blocks, cache
+        self.gamma, self.beta, self.eps, self.cos_sin = gamma, beta, eps, cos_sin
+        self.rope_offset, self.interleaved = rope_offset, interleaved
+        self.context_lens = torch.zeros(batch, **i32)
+        self.cu_new, self.cu_ctx, self.cu_blocks = (torch.zeros(batch + 1, **i32) for _ in range(3))
+        self.slot_mapping, self.positions = torch.full((rows,), -1, **i64), torch.zeros(rows, **i64)
+        self.row_req, self.row_len, self.ks, self.ke = (torch.zeros(rows, **i32) for _ in range(4))
+        self.q_rot = torch.empty(rows, heads, HEAD_DIM, dtype=torch.bfloat16, device=dev)
+        self.q_fp8 = torch.empty(rows, heads, HEAD_DIM, dtype=torch.uint8, device=dev)
+        self.w = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+
+    def run(self, cached_lens: torch.Tensor, new_lens: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+            w: torch.Tensor, stream=None) -> None:
+        """cached_lens, new_lens [B] int32; k [rows, 128] bf16, fp16 or f32; q [rows, heads, 128] bf16 (either may
+        be a slice of a fused projection); w [rows, heads] f32."""
+        ix_plan_step(cached_lens, new_lens, self.free_blocks, self.block_table, self.context_lens, self.cu_new,
+                     self.cu_ctx, self.cu_blocks, self.slot_mapping, self.positions, self.row_req, self.row_len,
+                     self.ks, self.ke, block_size=BLOCK_SIZE, stream=stream)
+        ix_norm_rope_write_k(k, self.gamma, self.beta, self.eps, self.positions, self.cos_sin, self.slot_mapping,
+                             self.cache, rope_offset=self.rope_offset, interleaved=self.interleaved, stream=stream)
+        ix_rope(q, self.positions, self.cos_sin, self.q_rot, offset=self.rope_offset, interleaved=self.interleaved,
+                stream=stream)
+        ix_quant_q(self.q_rot, w, self.q_fp8, self.w, stream=stream)

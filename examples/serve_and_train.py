@@ -1,0 +1,132 @@
+"""The indexer from request lengths: prompts, decode steps, and a training step of its key norm.
+
+    python examples/serve_and_train.py
+
+Three requests are admitted with their prompts, then decode together, one graph
+replay a step; after that the key norm's weights take a few steps of gradient
+descent.  Everything on the GPU runs in the package's kernels; torch holds the
+memory.  The library is built first if it is missing.
+"""
+from __future__ import annotations
+
+import os
+import sys
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import torch
+
+import deepseek_v3_sparse_gb300 as dsix
+from deepseek_v3_sparse_gb300 import build
+from deepseek_v3_sparse_gb300.frontend import FrontEnd
+
+TOPK, ROT, MAX_POS, EPS = 64, 64, 8192, 1e-6
+
+
+def serve(prompts=(300, 0, 129), decode_steps=70, seed=0):
+    """Returns the last decode step's selection and how many keys each request has."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    batch, total = len(prompts), sum(prompts)
+    width = (max(prompts) + decode_steps) // 64 + 1
+    pool = torch.randperm(batch * width, generator=g, device="cuda").int()
+    table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+    cache = torch.zeros(batch * width, 64 * 132, dtype=torch.uint8, device="cuda")
+    cos_sin = torch.empty(MAX_POS, ROT, device="cuda")
+    dsix.ix_rope_table(cos_sin, dsix.ix_rope_frequencies(ROT, scaling="yarn", factor=4.0, original=2048))
+    norm = dict(gamma=torch.ones(128, device="cuda"), beta=torch.zeros(128, device="cuda"), eps=EPS)
+
+    def projections(rows):
+        return (torch.randn(rows, 128, generator=g, device="cuda").bfloat16(),
+                torch.randn(rows, dsix.HEADS, 128, generator=g, device="cuda").bfloat16(),
+                torch.rand(rows, dsix.HEADS, generator=g, device="cuda"))
+
+    # the prompts, in one packed step
+    lens = torch.tensor(prompts, dtype=torch.int32, device="cuda")
+    front = FrontEnd(rows=total, block_table=table, free_blocks=pool, cache=cache, cos_sin=cos_sin, **norm)
+    front.run(torch.zeros_like(lens), lens, *projections(total))
+    keys, scales = torch.empty(total, 128, dtype=torch.uint8, device="cuda"), torch.empty(total, device="cuda")
+    logits = torch.empty(total, (max(prompts) + 3) // 4 * 4, device="cuda")
+    chosen = torch.empty(total, TOPK, dtype=torch.int32, device="cuda")
+    dsix.ix_gather_k(cache, table, front.cu_ctx, keys, scales)
+    dsix.ix_mqa_logits(front.q_fp8, front.w, keys, scales, front.ks, front.ke, logits)
+    dsix.ix_topk_to_global(logits, front.row_len, front.row_req, table, TOPK, chosen)
+
+    # decode: the same calls for a token of each request, captured once
+    used = sum((n + 63) // 64 for n in prompts)
+    cached, one = lens.clone(), torch.ones_like(lens)
+    free = torch.empty(batch, dtype=torch.int32, device="cuda")
+    step = FrontEnd(rows=batch, block_table=table, free_blocks=free, cache=cache, cos_sin=cos_sin, **norm)
+    k, q, w = projections(batch)
+    logits = torch.empty(batch, width * 64, device="cuda")
+    chosen = torch.empty(batch, TOPK, dtype=torch.int32, device="cuda")
+    work = torch.zeros(dsix.ix_topk_hist_workspace_size(batch), dtype=torch.uint8, device="cuda")
+
+    def decode(stream=None):
+        step.run(cached, one, k, q, w, stream=stream)
+        dsix.ix_paged_mqa_logits_topk(step.q_fp8.view(batch, 1, dsix.HEADS, 128), step.w, cache, step.context_lens,
+                                      table, logits, TOPK, chosen, work, stream=stream)
+
+    counts, graph = list(prompts), None
+    for _ in range(decode_steps):
+        free.copy_(pool[used:used + batch])
+        used += sum(n % 64 == 0 for n in counts)  # requests whose last block is full take another
+        for new, old in zip(projections(batch), (k, q, w)):
+            old.copy_(new)
+        if graph is None:
+            decode()  # the first step sets the kernels up
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+                decode(side)
+            torch.cuda.current_stream().wait_stream(side)
+        graph.replay()
+        cached += one
+        counts = [n + 1 for n in counts]
+    assert dsix.ix_device_status() == 0 and dsix.ix_prep_device_status() == 0
+    return chosen, counts
+
+
+def train(rows=4096, steps=10, rate=2e-3, seed=0):
+    """Fits the key norm's weights to keys of other weights; returns the losses."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, 128, generator=g, device="cuda").bfloat16()
+    positions = torch.randint(0, MAX_POS, (rows,), generator=g, device="cuda")
+    cos_sin = torch.empty(MAX_POS, ROT, device="cuda")
+    dsix.ix_rope_table(cos_sin, dsix.ix_rope_frequencies(ROT))
+    want_gamma = 1 + 0.5 * torch.randn(128, generator=g, device="cuda")
+    want_beta = 0.5 * torch.randn(128, generator=g, device="cuda")
+    gamma, beta = torch.ones(128, device="cuda"), torch.zeros(128, device="cuda")
+    y, z, target, dz, dx = (torch.empty_like(x) for _ in range(5))
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dgamma, dbeta = torch.empty(128, device="cuda"), torch.empty(128, device="cuda")
+    work = torch.empty(dsix.ix_layer_norm_bwd_workspace_size(rows, 128), dtype=torch.uint8, device="cuda")
+
+    def forward(gamma, beta, out):
+        dsix.ix_layer_norm(x, gamma, beta, EPS, y, mean, rstd)
+        dsix.ix_rope(y[:, None], positions, cos_sin, out[:, None])
+
+    forward(want_gamma, want_beta, target)
+    losses = []
+    for _ in range(steps):
+        forward(gamma, beta, z)
+        dz.copy_(z.float() - target.float())  # the gradient of half the squared distance
+        losses.append(float((dz.float() ** 2).sum()) / (2 * rows))
+        dsix.ix_rope(dz[:, None], positions, cos_sin, dz[:, None], inverse=True)  # in place
+        dsix.ix_layer_norm_bwd(dz, x, gamma, mean, rstd, dx, dgamma, dbeta, work)
+        gamma -= rate * 128 / rows * dgamma
+        beta -= rate * 128 / rows * dbeta
+    return losses
+
+
+def main():
+    build.build()
+    chosen, counts = serve()
+    print("keys per request:", counts)
+    print("selected in the last step:", [int((row >= 0).sum()) for row in chosen])
+    losses = train()
+    print("key norm's loss: %.3f -> %.3f" % (losses[0], losses[-1]))
+
+
+if __name__ == "__main__":
+    main()
