@@ -21,7 +21,6 @@
 // the first and the last vector of a row are cut.
 #pragma once
 
-#include <atomic>
 #include <initializer_list>
 
 #include "prep.cuh"
@@ -29,6 +28,7 @@
 namespace dsix {
 
 constexpr int kMaxCols = 32768;
+constexpr int kRowSmem = 200 * 1024;  // of the rows in flight, at most
 constexpr int kSms = 152;  // the grids' unit: whole multiples fill a GB300
 
 // a CTA of at least `least` threads: one row, or several at a time
@@ -73,19 +73,6 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*s)[32], int grou
             for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
 }
-
-// the first n of B bytes from global to shared memory, asynchronously, zeros behind them
-template <int B>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, uint32_t n) {
-    if constexpr (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(B), "r"(n)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Sums in pairs, of products too.  Vector u's elements go to partial sums in
 // turn, so that several independent additions are in flight; where a vector is a
@@ -133,22 +120,6 @@ struct Pairs {
         return s.x + s.y;
     }
 };
-
-// Shared memory beyond kPlainSmem has to be asked for, once for each kernel and
-// device; rows in flight take at most kRowSmem.
-constexpr int kPlainSmem = 46 * 1024, kRowSmem = 200 * 1024;
-template <auto kernel>
-int allow_smem(int bytes) {
-    static std::atomic<uint64_t> done{0};  // a bit per device
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return IX_ERR_CUDA;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (done.load(std::memory_order_relaxed) & bit) return IX_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return IX_ERR_CUDA;
-    done.fetch_or(bit, std::memory_order_relaxed);
-    return IX_OK;
-}
 
 template <int V>
 __device__ __forceinline__ void fill(float (&f)[V], float v) {

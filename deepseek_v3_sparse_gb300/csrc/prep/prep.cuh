@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "../../../include/dsix_prep.h"
 #include "../common.cuh"
 
@@ -103,6 +105,19 @@ __device__ __forceinline__ void load_f32(const float* p, float (&f)[V]) {
     }
 }
 
+// the first n of B bytes from global to shared memory, asynchronously, zeros behind them
+template <int B>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, uint32_t n) {
+    if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(B), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Division of n < 2^31 by a number known at launch: with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, n / d = (high word of n m + n) >> s
 // (T. Granlund and P. Montgomery, "Division by invariant integers using
@@ -116,6 +131,22 @@ struct FastDiv {
     }
     __device__ __forceinline__ uint32_t of(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
 };
+
+// Shared memory beyond kPlainSmem has to be asked for, once for each kernel and
+// device.
+constexpr int kPlainSmem = 46 * 1024;
+template <auto kernel>
+int allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return IX_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return IX_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return IX_ERR_CUDA;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return IX_OK;
+}
 
 inline bool aligned_to(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;

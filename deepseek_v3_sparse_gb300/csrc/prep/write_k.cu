@@ -1,12 +1,12 @@
 // write_k.cu -- ix_norm_rope_write_k: layer norm, rotary positions, fp8 coding
 // and the paged write of the indexer key, one pass over the token.
 //
-// Eight lanes hold a token, two vectors of eight values each, cut as ix_rope
-// cuts a head: rot / 16 lanes have eight whole pairs (half layout: a vector of
-// each half; interleaved: two adjacent vectors), the others two vectors of the
-// rest.  So no pair crosses a lane, and the three reductions of a token (mean,
-// centred squares, amax) are three shuffles each.  The next token's loads are in
-// flight behind the present one's arithmetic.
+// Eight lanes hold a token, two vectors of eight values each: rot / 16 lanes have
+// eight whole pairs (half layout: a vector of each half; interleaved: two adjacent
+// vectors), the others two vectors of the rest.  So no pair crosses a lane, and
+// the three reductions of a token (mean, centred squares, amax) are three shuffles
+// each.  The next token's loads are in flight behind the present one's
+// arithmetic, which is in pairs of f32 operations.
 #include <float.h>
 
 #include "prep.cuh"
@@ -19,7 +19,7 @@ constexpr int kBlock = 64;
 constexpr int kBlockBytes = kBlock * (kDim + 4);
 constexpr int kLanes = 8;             // per token
 constexpr int kPer = kDim / kLanes;   // values per lane
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kCtas = 4;  // of a CTA, CTAs of an SM
 
 struct WriteArgs {
     const void* k;
@@ -59,29 +59,32 @@ struct Token {
             hi[i] = live ? load_vec<T, V>(row + e1 + i * V) : zero_vec<T, V>();
         }
     }
-    __device__ __forceinline__ void unpack(float (&x)[kPer]) const {
+    __device__ __forceinline__ void unpack(float2 (&x)[kPer / 2]) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float f[V];
             lo[i].unpack(f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[i * V + j] = f[j];
+            for (int j = 0; j < V / 2; ++j) x[i * V / 2 + j] = make_float2(f[2 * j], f[2 * j + 1]);
             hi[i].unpack(f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) x[8 + i * V + j] = f[j];
+            for (int j = 0; j < V / 2; ++j) x[4 + i * V / 2 + j] = make_float2(f[2 * j], f[2 * j + 1]);
         }
     }
 };
 
-__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+__device__ __forceinline__ uint2 codes8(const float2* x, float inv) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cvt_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = __fmul2_rn(x[i], make_float2(inv, inv));
+        w[i] = cvt_e4m3x2(q.x, q.y);
+    }
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 template <class T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rope_write_kernel(const WriteArgs a) {
     const int lane = threadIdx.x & 31, sub = lane & (kLanes - 1);
     const int pair_lanes = a.rot / 16;
     const bool rotated = sub < pair_lanes;
@@ -90,33 +93,31 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_write_kernel(const Writ
         e0 = a.offset + (kInterleaved ? 16 : 8) * sub;
         e1 = kInterleaved ? e0 + 8 : e0 + a.rot / 2;
     } else {
-        const int v = 16 * (sub - pair_lanes);
+        // the rest of the key, in two runs of vectors: neighbouring lanes have neighbouring ones
+        const int v = 8 * (sub - pair_lanes), w = v + 8 * (kLanes - pair_lanes);
         e0 = v < a.offset ? v : v + a.rot;
-        e1 = v + 8 < a.offset ? v + 8 : v + 8 + a.rot;
+        e1 = w < a.offset ? w : w + a.rot;
     }
     const int64_t tokens = (static_cast<int64_t>(gridDim.x) * kThreads) / kLanes;
     int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
     Token<T> next;
     next.load(a, t, e0, e1);
-    float g[kPer], b[kPer];
+    float2 g[kPer / 2], b[kPer / 2];
     {
         float f[8];
-        load_f32<8>(a.gamma + e0, f);
+        auto take = [&](const float* w, float2* to) {
+            load_f32<8>(w, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = f[i];
-        load_f32<8>(a.gamma + e1, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[8 + i] = f[i];
-        load_f32<8>(a.beta + e0, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = f[i];
-        load_f32<8>(a.beta + e1, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[8 + i] = f[i];
+            for (int i = 0; i < 4; ++i) to[i] = make_float2(f[2 * i], f[2 * i + 1]);
+        };
+        take(a.gamma + e0, g);
+        take(a.gamma + e1, g + 4);
+        take(a.beta + e0, b);
+        take(a.beta + e1, b + 4);
     }
     // the loop runs for the warp's first token, so that all lanes meet in the shuffles
     for (; t - (lane / kLanes) < a.n; t += tokens) {
-        float x[kPer];
+        float2 x[kPer / 2];
         next.unpack(x);
         const int64_t slot = next.slot, pos = next.pos;
         const int64_t blk = slot / kBlock;
@@ -132,32 +133,39 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_write_kernel(const Writ
             load_f32<8>(row + a.rot / 2, s);
         }
         next.load(a, t + tokens, e0, e1);
-        float sum = 0.f;
+        float2 sum = x[0];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sum += x[i];
-        const float mean = sum8(sum) * (1.f / kDim);
-        float sq = 0.f;
+        for (int i = 1; i < kPer / 2; ++i) sum = __fadd2_rn(sum, x[i]);
+        const float mean = sum8(sum.x + sum.y) * (1.f / kDim);
+        float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            x[i] -= mean;
-            sq = fmaf(x[i], x[i], sq);
+        for (int i = 0; i < kPer / 2; ++i) {
+            x[i] = __fadd2_rn(x[i], make_float2(-mean, -mean));
+            sq = __ffma2_rn(x[i], x[i], sq);
         }
-        const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sum8(sq), 1.f / kDim, a.eps)));
+        const float rstd = rsqrtf(fmaf(sum8(sq.x + sq.y), 1.f / kDim, a.eps));
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = fmaf(x[i] * rstd, g[i], b[i]);
+        for (int i = 0; i < kPer / 2; ++i) x[i] = __ffma2_rn(__fmul2_rn(x[i], make_float2(rstd, rstd)), g[i], b[i]);
         if (write && rotated) {
+            if constexpr (kInterleaved) {  // x[i] is pair i
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float& p = x[kInterleaved ? 2 * i : i];
-                float& q = x[kInterleaved ? 2 * i + 1 : 8 + i];
-                const float y = p;
-                p = fmaf(-q, s[i], y * c[i]);
-                q = fmaf(y, s[i], q * c[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float2 p = x[i];
+                    x[i] = make_float2(fmaf(-p.y, s[i], p.x * c[i]), fmaf(p.x, s[i], p.y * c[i]));
+                }
+            } else {  // x[i] and x[4 + i] are two pairs
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p = x[i], q = x[4 + i];
+                    const float2 ci = make_float2(c[2 * i], c[2 * i + 1]), si = make_float2(s[2 * i], s[2 * i + 1]);
+                    x[i] = __ffma2_rn(make_float2(-q.x, -q.y), si, __fmul2_rn(p, ci));
+                    x[4 + i] = __ffma2_rn(p, si, __fmul2_rn(q, ci));
+                }
             }
         }
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) amax = fmaxf(amax, fabsf(x[i]));
+        for (int i = 0; i < kPer / 2; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float scale = fmaxf(__fdiv_rn(amax, 448.f), FLT_MIN);
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_write_kernel(const Writ
             const int at = static_cast<int>(slot % kBlock);
             uint8_t* base = a.cache + blk * kBlockBytes;
             *reinterpret_cast<uint2*>(base + at * kDim + e0) = codes8(x, inv);
-            *reinterpret_cast<uint2*>(base + at * kDim + e1) = codes8(x + 8, inv);
+            *reinterpret_cast<uint2*>(base + at * kDim + e1) = codes8(x + 4, inv);
             if (sub == 0) *reinterpret_cast<float*>(base + kBlock * kDim + 4 * at) = scale;
         }
     }
@@ -208,7 +216,7 @@ extern "C" int ix_norm_rope_write_k(const void* k, int64_t k_stride, int dtype, 
     if (!st || sms <= 0) return IX_ERR_CUDA;
     const WriteArgs a{k, k_stride, n, gamma, beta, eps, positions, cos_sin, max_pos, rot, offset,
                       slot_mapping, cache, num_blocks, st};
-    const int64_t want = (n + kThreads / kLanes - 1) / (kThreads / kLanes), cap = static_cast<int64_t>(sms) * 2;
+    const int64_t want = (n + kThreads / kLanes - 1) / (kThreads / kLanes), cap = static_cast<int64_t>(sms) * kCtas;
     const int grid = static_cast<int>(want < cap ? want : cap);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == IX_BF16)
