@@ -32,8 +32,8 @@ struct Bwd : RowShape<G, 512> {
     using Shape = RowShape<G, 512>;
     static constexpr int E = U * V, bytes = V * sizeof(T);
     // gamma stays in registers from row to row, and h and xhat from the row's sums to
-    // its dx, as long as the threads of the widest rows have them
-    static constexpr bool hold = G < 1024;
+    // its dx, where a thread has few enough columns
+    static constexpr bool hold = E <= 16 && G < 1024;
     static constexpr int slots = 2 * U;     // of a thread and stage: x, then dy
     static constexpr int row = Shape::threads * slots * bytes;
     // rows in shared memory: the present one and the next ones on their way (none
@@ -323,7 +323,9 @@ int launch(const BwdArgs& a, int* parts, cudaStream_t s) {
 
 constexpr int kFusedCols = 16384, kFusedScattered = 8192;  // with column sums
 
-// 16 elements a thread: their sums, twice, and gamma leave registers for the rest
+// 16 elements a thread: their sums, twice, and gamma leave registers for the rest;
+// the widest rows have 32, without gamma (1024 threads have 64 registers, which
+// spill)
 template <class T, bool kSums, bool kShift>
 int by_width(const BwdArgs& a, int* parts, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T), U = 16 / W;
@@ -335,7 +337,7 @@ int by_width(const BwdArgs& a, int* parts, cudaStream_t s) {
     if (n <= 2048) return launch<T, W, 128, U, kSums, kShift>(a, parts, s);
     if (n <= 4096) return launch<T, W, 256, U, kSums, kShift>(a, parts, s);
     if (n <= 8192) return launch<T, W, 512, U, kSums, kShift>(a, parts, s);
-    if (n <= kFusedCols) return launch<T, W, 1024, U, kSums, kShift>(a, parts, s);
+    if (n <= kFusedCols) return launch<T, W, 512, 2 * U, kSums, kShift>(a, parts, s);
     if constexpr (!kSums) return launch<T, kShift ? 1 : W, 1024, kShift ? 32 : 2 * U, false>(a, parts, s);
     return IX_ERR_UNSUPPORTED;
 }

@@ -1,5 +1,7 @@
 // rope.cu -- rotary positions: the frequencies (host), the table, and the
 // rotation of a part of every head.
+#include <type_traits>
+
 #include "prep.cuh"
 
 namespace dsix {
@@ -277,20 +279,30 @@ int launch(RopeArgs& a, int dim, bool copies, bool interleaved, cudaStream_t s) 
 
 template <class T>
 int dispatch(RopeArgs& a, int dim, bool copies, bool interleaved, int sms, cudaStream_t s) {
-    constexpr int W = 16 / sizeof(T);
-    // 16-byte vectors where every pointer, stride and part of the head allows them
-    bool wide = a.offset % W == 0 && (a.rot / 2) % W == 0 && aligned16(a.cos_sin) &&
-                (!copies || (dim - a.offset - a.rot) % W == 0);
-    for (const RopeSide& d : a.side)
-        if (d.x)
-            wide = wide && aligned16(d.x) && aligned16(d.out) && d.xt % W == 0 && d.ot % W == 0 &&
-                   (d.heads == 1 || (d.xh % W == 0 && d.oh % W == 0));
+    // the widest vectors, up to 16 bytes, that every pointer, stride and part of the head allows
+    auto fits = [&](int v) {
+        const int bytes = v * static_cast<int>(sizeof(T));
+        bool ok = a.offset % v == 0 && (a.rot / 2) % v == 0 && (v % 4 || aligned16(a.cos_sin)) &&
+                  (!copies || (dim - a.offset - a.rot) % v == 0);
+        for (const RopeSide& d : a.side)
+            if (d.x)
+                ok = ok && aligned_to(d.x, bytes) && aligned_to(d.out, bytes) && d.xt % v == 0 && d.ot % v == 0 &&
+                     (d.heads == 1 || (d.xh % v == 0 && d.oh % v == 0));
+        return ok;
+    };
     const int64_t values = a.tokens * a.side[0].heads * dim;
     // four heads a thread once that leaves every SM its share of threads
     const bool many = values * static_cast<int64_t>(sizeof(T)) >= static_cast<int64_t>(sms) * 2048 * 128;
-    if (wide)
-        return many ? launch<T, W, 4>(a, dim, copies, interleaved, s) : launch<T, W, 1>(a, dim, copies, interleaved, s);
-    return many ? launch<T, 1, 4>(a, dim, copies, interleaved, s) : launch<T, 1, 1>(a, dim, copies, interleaved, s);
+    auto go = [&](auto width) {
+        constexpr int V = decltype(width)::value;
+        return many ? launch<T, V, 4>(a, dim, copies, interleaved, s) : launch<T, V, 1>(a, dim, copies, interleaved, s);
+    };
+    if constexpr (sizeof(T) == 2) {
+        if (fits(8)) return go(std::integral_constant<int, 8>());
+    }
+    if (fits(4)) return go(std::integral_constant<int, 4>());
+    if (fits(2)) return go(std::integral_constant<int, 2>());
+    return go(std::integral_constant<int, 1>());
 }
 
 // an output whose elements are all distinct: heads within tokens, or tokens within heads
