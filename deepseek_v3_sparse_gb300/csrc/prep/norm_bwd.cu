@@ -38,12 +38,17 @@ struct Bwd : RowShape<G, 512> {
     static constexpr int row = Shape::threads * slots * bytes;
     // rows in shared memory: the present one and the next ones on their way (none
     // where one would not fit)
-    static constexpr int stages = kRowSmem / row < 4 ? kRowSmem / row : 4;
+    // without registers for gamma, each thread's columns of it lie there too, as f32,
+    // unless a row would not fit beside them
+    static constexpr int gamma_bytes = Shape::threads * E * static_cast<int>(sizeof(float));
+    static constexpr bool gamma_near = !hold && V % 4 == 0 && kRowSmem - gamma_bytes >= row;
+    static constexpr int gamma_smem = gamma_near ? gamma_bytes : 0;
+    static constexpr int stages = (kRowSmem - gamma_smem) / row < 4 ? (kRowSmem - gamma_smem) / row : 4;
     static constexpr bool async = bytes >= 4 && stages > 0;
     // the CTA's column sums of one weight, row by row, take the rows' place in the end
     static constexpr int cols = G * E, sums_smem = Shape::rows * cols * static_cast<int>(sizeof(float));
     static constexpr int rows_smem = async ? stages * row : 0;
-    static constexpr int smem = rows_smem < sums_smem ? sums_smem : rows_smem;
+    static constexpr int smem = rows_smem + gamma_smem < sums_smem ? sums_smem : rows_smem + gamma_smem;
 };
 
 template <class T, int V, int G, int U, bool kSums, bool kShift>
@@ -90,10 +95,34 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
         fill<F::E>(ag, 0.f);
         fill<F::E>(ab, 0.f);
     }
-    auto weight = [&](int u, int c) { load_weight<T, V, kShift>(a.gamma, a.weight_f32, c, a.cols, 1.f, g[u]); };
+    float4* s_gamma = reinterpret_cast<float4*>(s_rows + F::rows_smem) + threadIdx.x;  // this thread's, F::threads apart
+    auto weight = [&](int to, int u) {  // gamma of vector u
+        if constexpr (F::gamma_near) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 q = s_gamma[(u * (V / 4) + i) * F::threads];
+                g[to][4 * i] = q.x;
+                g[to][4 * i + 1] = q.y;
+                g[to][4 * i + 2] = q.z;
+                g[to][4 * i + 3] = q.w;
+            }
+        } else {
+            load_weight<T, V, kShift>(a.gamma, a.weight_f32, c0 + u * G * V, a.cols, 1.f, g[to]);
+        }
+    };
     if constexpr (F::hold) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) weight(u, c0 + u * G * V);
+        for (int u = 0; u < U; ++u) weight(u, u);
+    }
+    if constexpr (F::gamma_near) {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            float w[V];
+            load_weight<T, V, kShift>(a.gamma, a.weight_f32, c0 + u * G * V, a.cols, 1.f, w);
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i)
+                s_gamma[(u * (V / 4) + i) * F::threads] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
     }
     int stage = 0, flip = 0;  // the sums of consecutive rows use other places: one barrier a row is enough
     for (; r0 < a.rows; r0 += step) {
@@ -142,7 +171,7 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
         // (without a test of the column: outside of the row dy = 0)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if constexpr (!F::hold) weight(0, c0 + u * G * V);
+            if constexpr (!F::hold) weight(0, u);
             const float(&w)[V] = g[u * keep];
             float(&x)[V] = xs[u * keep];
             float(&h)[V] = hs[u * keep];
@@ -192,7 +221,7 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
                 float(&h)[V] = hs[u * keep];
                 float d[V];
                 if constexpr (!F::hold) {
-                    weight(0, c);
+                    weight(0, u);
                     read(u, x, d);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
