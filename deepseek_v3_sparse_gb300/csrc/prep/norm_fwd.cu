@@ -3,6 +3,11 @@
 // The row is copied to shared memory once and read there by the three passes over
 // it: the sum, the sum of the centred squares (no cancellation, whatever the
 // mean), the output.
+//
+// Bound by DRAM: 8192 x 4096 bf16 in 22.4 us, 6.0 TB/s, 88% of a copy's rate.  With
+// a row to 256 threads and 16 elements each it took 37.6 us, bound by the issue of
+// the rows' sums; with the weights read from L1 for every row 46 us.  Rows of an
+// odd width pay for their cut vectors: 8192 x 4001 bf16 in 31 us.
 #include "norm.cuh"
 
 namespace dsix {

@@ -7,6 +7,13 @@
 // the three reductions of a token (mean, centred squares, amax) are three shuffles
 // each.  The next token's loads are in flight behind the present one's
 // arithmetic, which is in pairs of f32 operations.
+//
+// Measured: 65521 tokens of 128 bf16 in 12.0 us, of which reading and norming them
+// without a write is 7.1 us and the rest are the rotary rows (256 bytes a token) and
+// the scattered stores; 32760 tokens, which stay in L2, in 5.8 us; 256 in 2.0 us.
+// Four CTAs of 128 threads to an SM with gamma and beta in registers; eight CTAs of
+// 64 registers with both in shared memory took 14.4 us, asynchronous copies of keys
+// and rotary rows 12.5 us.
 #include <float.h>
 
 #include "prep.cuh"
