@@ -166,6 +166,23 @@ def test_the_inverse_is_the_gradient(dsix):
         assert abs(quotient - float((v.double() * grad).sum())) <= 2 * tol
 
 
+def test_more_items_than_one_launch_indexes(dsix):
+    """65536 heads of 128 values in single elements: a launch takes 1024 tokens, so
+    1030 go out in two, the second at an offset past 2^32 elements.  The input is
+    one token's, broadcast."""
+    heads, dim, tokens = 65536, 128, 1030
+    x = torch.randn(1, heads, dim, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    out = torch.empty(tokens, heads, dim, dtype=torch.bfloat16, device="cuda")
+    table = torch.empty(tokens, 2, device="cuda")
+    dsix.ix_rope_table(table, [0.01])
+    pos = torch.arange(tokens, device="cuda").flip(0).contiguous()
+    dsix.ix_rope(x.expand(tokens, heads, dim), pos, table, out, offset=3)
+    assert dsix.ix_prep_device_status() == 0
+    for t in (0, 1, 1022, 1023, 1024, 1025, 1029):
+        want, size = reference(x, pos[t:t + 1], table, 3, False, False)
+        close(out[t:t + 1], want, size, 2)
+
+
 def test_bad_positions_are_skipped(dsix):
     table = torch.ones(8, 64, device="cuda")
     x = torch.randn(4, 3, 128, device="cuda")
