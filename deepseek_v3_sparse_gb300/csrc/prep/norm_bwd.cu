@@ -317,28 +317,37 @@ __global__ void __launch_bounds__(kColThreads) norm_cols_kernel(const BwdArgs a)
     part[a.cols + c] = b;
 }
 
-// the parts' sums, in their order: 32 columns a CTA, 32 threads a column
-__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* part, int parts, int cols, float* dgamma,
-                                                          float* dbeta) {
-    __shared__ float s[32][33];
+// the parts' sums, in their order: 32 columns a CTA, kDown threads a column, each
+// with all its loads in flight
+constexpr int kDown = 16, kEach = (kParts + kDown - 1) / kDown;
+__global__ void __launch_bounds__(32 * kDown) norm_parts_kernel(const float* part, int parts, int cols, float* dgamma,
+                                                                float* dbeta) {
+    __shared__ float s[kDown][33];
+    const int x = threadIdx.x, y = threadIdx.y;
+    const int i = blockIdx.x * 32 + x;  // column of [dgamma | dbeta]
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched early: the parts are whole only now
-    const int i = blockIdx.x * 32 + threadIdx.x;  // column of [dgamma | dbeta]
-    float v = 0.f;
-    if (i < 2 * cols) {
-#pragma unroll 4
-        for (int p = threadIdx.y; p < parts; p += 32) v += part[static_cast<int64_t>(p) * 2 * cols + i];
-    }
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    v = s[threadIdx.x][threadIdx.y];  // thread (x, y): part x of column y
+    float v[kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int j = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && j < 2 * cols) {
+    for (int k = 0; k < kEach; ++k) {
+        const int p = y + k * kDown;
+        v[k] = i < 2 * cols && p < parts ? part[static_cast<int64_t>(p) * 2 * cols + i] : 0.f;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) sum += v[k];
+    s[y][x] = sum;
+    __syncthreads();
+    // half a warp for each column
+    const int column = 2 * y + x / kDown;
+    sum = s[x % kDown][column];
+#pragma unroll
+    for (int o = kDown / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int j = blockIdx.x * 32 + column;
+    if (x % kDown == 0 && j < 2 * cols) {
         if (j < cols)
-            dgamma[j] = v;
+            dgamma[j] = sum;
         else
-            dbeta[j - cols] = v;
+            dbeta[j - cols] = sum;
     }
 }
 
@@ -419,7 +428,7 @@ int dispatch(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t s) {
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t config{};
     config.gridDim = dim3((2 * a.cols + 31) / 32);
-    config.blockDim = dim3(32, 32);
+    config.blockDim = dim3(32, kDown);
     config.stream = s;
     config.attrs = &early;
     config.numAttrs = 1;
