@@ -8,12 +8,12 @@
 // the row take their column sums in a pass of their own.
 //
 // Bound by DRAM up to 8192 columns: 8192 x 4096 bf16 in 36.7 us, 5.5 TB/s, 81% of a
-// copy's rate; 131071 x 128 bf16 in 20.0 us (75%), of which the second kernel is
-// 2 us.  What it took, at 8192 x 4096: one CTA a row and three to an SM 63 us; rows
-// of 512 threads' CTAs 45.5 us; h and xhat kept and mean and rstd copied ahead with
+// copy's rate; 131071 x 128 bf16 in 20.1 us (75%), of which the second kernel is
+// about 2 us.  What it took, at 8192 x 4096: CTAs of one row and 128 threads, two to
+// an SM, 63 us; CTAs of 512 threads 45.5 us; h and xhat kept and mean and rstd copied ahead with
 // their row (loaded by each thread they came late) 37.6 us.  Beyond 4096 columns a
 // CTA has one row and waits for its sums: 4099 x 5001 f32, whose vectors are cut
-// besides, 50 us (72%).
+// besides, 49.7 us (73%).
 #include "norm.cuh"
 
 namespace dsix {

@@ -10,9 +10,9 @@
 // redundant sums would cost more than a second launch: one CTA writes them, and
 // the rows search them in global memory.
 //
-// Measured in a graph: 4.3 us for 128 requests of two rows, of which 1.7 us are an
-// empty launch and the rest the chain lengths -> sums -> request -> table entry ->
-// slot; 11.6 us for 1024 prompts of 1.02M rows, whose 32 bytes of output a row
+// Measured in a graph: 4.4 us for 128 requests of two rows, of which 1.7 us are what
+// the smallest kernel takes and the rest the chain lengths -> sums -> request ->
+// table entry -> slot; 11.5 us for 1024 prompts of 1.02M rows, whose 32 bytes of output a row
 // need 8.4 us even when every row is empty.  A CTA has 512 threads of up to 64
 // registers, two to an SM: three CTAs of 40 registers took 14.7 us and single
 // ones of 1024 threads 13.3 us.  Four rows a thread are planned together, with

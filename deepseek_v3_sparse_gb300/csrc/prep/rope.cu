@@ -139,8 +139,8 @@ uint64_t turns_of(double f) {
 // neighbouring vectors.  Indexes have 31 bits and are divided by multiplication.
 // Bound by DRAM: 8192 x (64 + 1) x 128 bf16, half of every head turned, in 41.0 us,
 // 6.7 TB/s, 99% of a copy's rate (121 us with 64-bit divisions and warps that both
-// turn and copy).  With 2-byte elements alone (a head of 77) it is bound by
-// instructions: 27% of that rate.
+// turn and copy).  A head of 77 values, which only 2-byte accesses fit, reaches 27%
+// of that rate.
 // ---------------------------------------------------------------------------
 struct RopeSide {
     const void* x;
