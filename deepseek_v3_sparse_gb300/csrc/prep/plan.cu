@@ -10,9 +10,8 @@
 // redundant sums would cost more than a second launch: one CTA writes them, and
 // the rows search them in global memory.
 //
-// Measured in a graph: 4.4 us for 128 requests of two rows, of which 1.7 us are what
-// the smallest kernel takes and the rest the chain lengths -> sums -> request ->
-// table entry -> slot; 11.5 us for 1024 prompts of 1.02M rows, whose 32 bytes of output a row
+// Measured in a graph: FEW us for 128 requests of two rows (4.4 us before a request's
+// thread planned its rows), of which 1.7 us are what the smallest kernel takes; 11.5 us for 1024 prompts of 1.02M rows, whose 32 bytes of output a row
 // need 8.4 us even when every row is empty.  A CTA has 512 threads of up to 64
 // registers, two to an SM: three CTAs of 40 registers took 14.7 us and single
 // ones of 1024 threads 13.3 us.  Four rows a thread are planned together, with
@@ -173,10 +172,23 @@ __device__ __forceinline__ void store4(int64_t* to, const int64_t (&v)[kRows], b
     }
 }
 
+// the block that request b's block j is, from the table or, past the request's
+// `have` blocks, from the free list behind its first entry there; -1, and a bit, where there is none
+__device__ __forceinline__ int32_t block_at(const PlanArgs& a, int b, int32_t j, int32_t have, int64_t first_free) {
+    if (j >= a.width) {
+        flag(a.status, IX_DEV_BAD_RANGE);
+        return -1;
+    }
+    if (j >= have) return free_block(a, first_free + (j - have));
+    const int32_t block = a.table[b * a.stride + j];
+    if (block < 0) flag(a.status, IX_DEV_BAD_BLOCK);
+    return block;
+}
+
 // rows and new blocks, from the sums cn, cc, cb
 __device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, const int32_t* cb) {
-    const int64_t threads = static_cast<int64_t>(gridDim.x) * kThreads;
-    const int64_t tid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t threads = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int32_t total = a.batch ? cn[a.batch] : 0;
     if (tid == 0 && total > a.rows) flag(a.status, IX_DEV_BAD_RANGE);
     for (int64_t t0 = tid * kRows; t0 < a.rows; t0 += threads * kRows) {
@@ -210,15 +222,7 @@ __device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, 
             const int32_t j = static_cast<int32_t>(div_block(a, static_cast<uint32_t>(p)));
             if (j != block_of) {
                 block_of = j;
-                block = -1;
-                if (j >= a.width) {
-                    flag(a.status, IX_DEV_BAD_RANGE);
-                } else if (j < have) {
-                    block = a.table[b * a.stride + j];
-                    if (block < 0) flag(a.status, IX_DEV_BAD_BLOCK);
-                } else {
-                    block = free_block(a, static_cast<int64_t>(cb[b]) + (j - have));
-                }
+                block = block_at(a, b, j, have, cb[b]);
             }
             if (block >= 0)
                 slot[i] = static_cast<int64_t>(block) * a.block_size +
@@ -278,6 +282,120 @@ __global__ void __launch_bounds__(kThreads) plan_fused_kernel(const PlanArgs a) 
     expand(a, cn, cc, cb);
 }
 
+// Small steps: a request to a thread, which plans the request's rows itself where
+// every request has a few (decode steps), without a search and under one barrier;
+// the table entry of its first row is on its way while the sums are formed.  Every
+// CTA forms all sums; kShare requests' rows are its own (one SM alone would take
+// 6.8 us to store the 2048 rows of 512 requests).
+constexpr int kFew = 8, kFewThreads = 1024, kShare = 64;
+__global__ void __launch_bounds__(kFewThreads) plan_few_kernel(const PlanArgs a) {
+    extern __shared__ int32_t s_sums[];
+    __shared__ Sums s_warp[kFewThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = threadIdx.x;
+    const bool live = b < a.batch;
+    const int32_t c = live ? __ldg(a.cached + b) : 0, n = live ? __ldg(a.fresh + b) : 0;
+    const uint32_t uc = max(c, 0), un = max(n, 0), all = add_sat(uc, un);
+    const int32_t have = static_cast<int32_t>(blocks_of(a, uc)), lack = static_cast<int32_t>(blocks_of(a, all)) - have;
+    const int32_t j0 = static_cast<int32_t>(div_block(a, uc));
+    const bool mine = live && b / kShare == static_cast<int>(blockIdx.x);
+    const bool begun = mine && un > 0 && j0 < have && j0 < a.width;  // the first row's block holds tokens already
+    const int32_t block0 = begun ? a.table[b * a.stride + j0] : -1;
+    Sums inc{un, all, static_cast<uint32_t>(lack)};
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const Sums o = shfl_up(inc, d);
+        if (lane >= d) inc = inc + o;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    const bool many = __syncthreads_or(un > kFew);
+    Sums ex = shfl_up(inc, 1), total{0, 0, 0};
+    if (lane == 0) ex = {0, 0, 0};
+    const int warps = (a.batch + 31) / 32;
+    if (warps <= 8) {
+#pragma unroll 1
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) ex = total + ex;
+            total = total + s_warp[w];
+        }
+    } else {  // a lane to a warp's sum
+        Sums sum{0, 0, 0};
+        if (lane < warps) sum = s_warp[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sums o = shfl_up(sum, d);
+            if (lane >= d) sum = sum + o;
+        }
+        auto at = [&](int l) {
+            return Sums{__shfl_sync(0xffffffffu, sum.n, l), __shfl_sync(0xffffffffu, sum.c, l),
+                        __shfl_sync(0xffffffffu, sum.b, l)};
+        };
+        const Sums before = at(warp ? warp - 1 : 0);
+        if (warp) ex = before + ex;
+        total = at(31);
+    }
+    bool bad = c < 0 || n < 0 || uc + un > kMax;
+    auto publish = [&](int i, const Sums& at, bool write) {
+        if (write) {
+            a.cu_new[i] = static_cast<int32_t>(at.n);
+            a.cu_ctx[i] = static_cast<int32_t>(at.c);
+            a.cu_blocks[i] = static_cast<int32_t>(at.b);
+        }
+        if (many) {
+            s_sums[i] = static_cast<int32_t>(at.n);
+            s_sums[a.batch + 1 + i] = static_cast<int32_t>(at.c);
+            s_sums[2 * (a.batch + 1) + i] = static_cast<int32_t>(at.b);
+        }
+    };
+    if (live) publish(b, ex, mine);
+    if (mine) a.context_lens[b] = static_cast<int32_t>(all);
+    if (b == 0) {
+        publish(a.batch, total, blockIdx.x == 0);
+        bad |= total.n == kMax || total.c == kMax || total.b == kMax || total.n > a.rows;
+    }
+    if (bad) flag(a.status, IX_DEV_BAD_RANGE);
+    if (many) {
+        __syncthreads();
+        expand(a, s_sums, s_sums + a.batch + 1, s_sums + 2 * (a.batch + 1));
+        return;
+    }
+    int32_t block_of = begun ? j0 : -1, block = block0;
+    for (uint32_t i = 0; mine && i < un; ++i) {
+        const int64_t t = static_cast<int64_t>(ex.n) + i, p = static_cast<int64_t>(uc) + i;
+        if (t >= a.rows) break;
+        const bool row = p < static_cast<int64_t>(kMax);  // else a context past INT32_MAX, flagged above
+        int64_t slot = -1;
+        if (row) {
+            const int32_t j = static_cast<int32_t>(div_block(a, static_cast<uint32_t>(p)));
+            if (j != block_of) {
+                block_of = j;
+                block = block_at(a, b, j, have, ex.b);
+            } else if (i == 0 && block < 0) {
+                flag(a.status, IX_DEV_BAD_BLOCK);
+            }
+            if (block >= 0)
+                slot = static_cast<int64_t>(block) * a.block_size + (p - static_cast<int64_t>(j) * a.block_size);
+        }
+        a.slots[t] = slot;
+        a.positions[t] = row ? p : 0;
+        a.row_req[t] = row ? b : 0;
+        a.row_len[t] = row ? static_cast<int32_t>(p + 1) : 0;
+        a.ks[t] = row ? static_cast<int32_t>(ex.c) : 0;
+        a.ke[t] = row ? static_cast<int32_t>(add_sat(ex.c, static_cast<uint32_t>(p + 1))) : 0;
+    }
+    for (int32_t k = 0; mine && k < lack; ++k) {
+        if (have + k < a.width)
+            a.table[b * a.stride + have + k] = free_block(a, static_cast<int64_t>(ex.b) + k);
+        else
+            flag(a.status, IX_DEV_BAD_RANGE);
+    }
+    const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    for (int64_t t = total.n + tid; t < a.rows; t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        a.slots[t] = -1;
+        a.positions[t] = 0;
+        a.row_req[t] = a.row_len[t] = a.ks[t] = a.ke[t] = 0;
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) plan_scan_kernel(const PlanArgs a) {
     scan_requests(a, a.cu_new, a.cu_ctx, a.cu_blocks, true);
 }
@@ -321,6 +439,14 @@ extern "C" int ix_plan_step(const int32_t* cached_lens, const int32_t* new_lens,
     const int64_t want = (rows + kThreads * kRows - 1) / (kThreads * kRows);
     const int grid = static_cast<int>(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (batch <= kFewThreads && rows <= kFewThreads * kRows) {
+        const int threads = batch <= 256 ? 256 : batch <= 512 ? 512 : kFewThreads;
+        const int shares = (batch + kShare - 1) / kShare;
+        const int ctas = static_cast<int>((rows + threads * kRows - 1) / (threads * kRows));
+        const int few = shares > ctas ? shares : ctas < 1 ? 1 : ctas;
+        plan_few_kernel<<<few, threads, 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1), s>>>(a);
+        return launch_status();
+    }
     if (batch <= kFusedBatch) {
         const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(batch) + 1);
         if (smem > 48 * 1024 - sizeof(Sums) * (kThreads / 32) &&

@@ -138,6 +138,20 @@ def test_ragged_batches(dsix, B, hi, seed):
     check(dsix, cached, new)
 
 
+@pytest.mark.parametrize("B", [1, 31, 32, 33, 256, 257, 511, 512, 513, 1023, 1024, 1025])
+@pytest.mark.parametrize("hi", [1, 8, 9])
+def test_steps_of_few_rows(dsix, B, hi):
+    """Decode steps: a thread plans the rows of a request with up to eight; one request
+    with more sends the step the other way."""
+    g = torch.Generator().manual_seed(B + hi)
+    new = torch.randint(0, hi + 1, (B,), generator=g).tolist()
+    cached = torch.randint(0, 300, (B,), generator=g).tolist()
+    new[B // 2] = hi
+    check(dsix, cached, new, bs=16)
+    check(dsix, cached, new, bs=64, rows=sum(new) + 300)
+    check(dsix, cached, new, bs=3, rows=max(1, sum(new) // 2))
+
+
 def test_long_contexts(dsix):
     # positions and slots of a cache past 2^31 keys: the slot is formed in 64 bits
     width = 5
