@@ -1,21 +1,24 @@
 // plan.cu -- ix_plan_step: block tables, slot maps and row ranges from lengths.
 //
 // Three prefix sums over the requests (new tokens, whole contexts, missing
-// blocks), then one independent piece of arithmetic per row and per new block,
-// which finds its request by a binary search in the sums.  A step plans a few
-// kilobytes to a few tens of megabytes, so what counts is the number of
-// dependent round trips: up to kFusedBatch requests, every CTA forms the sums
-// itself in shared memory (8 bytes a request, from L2) and goes on to its rows
-// at once, in one launch and without a wait between CTAs.  Above that the
-// redundant sums would cost more than a second launch: one CTA writes them, and
-// the rows search them in global memory.
+// blocks), then one independent piece of arithmetic per row and per new block.
+// A step plans a few kilobytes to a few tens of megabytes, so what counts is the
+// number of dependent round trips.  Up to kFusedBatch requests, every CTA forms
+// the sums itself in shared memory (8 bytes a request, from L2) and goes on to its
+// rows at once, in one launch and without a wait between CTAs; a row finds its
+// request by a binary search in the sums.  Above that the redundant sums would
+// cost more than a second launch: one CTA writes them, and the rows search them in
+// global memory.  Small steps whose requests bring a few rows each (decode steps)
+// need no search: a request's thread plans its rows.
 //
-// Measured in a graph: FEW us for 128 requests of two rows (4.4 us before a request's
-// thread planned its rows), of which 1.7 us are what the smallest kernel takes; 11.5 us for 1024 prompts of 1.02M rows, whose 32 bytes of output a row
-// need 8.4 us even when every row is empty.  A CTA has 512 threads of up to 64
-// registers, two to an SM: three CTAs of 40 registers took 14.7 us and single
-// ones of 1024 threads 13.3 us.  Four rows a thread are planned together, with
-// their loads in flight at the same time; rows one after the other took 16.9 us.
+// Measured in a graph: 2.4 us for 128 requests of two rows (4.4 us with the
+// search), of which 1.7 us are what the smallest kernel takes; 3.2 us for 1024
+// requests of one; 11.1 us for 1024 prompts of 1.02M rows, whose 32 bytes of output
+// a row need 7.9 us even when every row is empty.  A CTA of that kernel has 512
+// threads of up to 64 registers, two to an SM: three CTAs of 40 registers took 14.7
+// us and single ones of 1024 threads 13.3 us.  Four rows a thread are planned
+// together, with their loads in flight at the same time; one after the other they
+// took 16.9 us.
 //
 // The sums saturate at INT32_MAX.  Saturating addition of non-negative numbers
 // is associative (both orders give min(sum, INT32_MAX)), so 32-bit scans in any
@@ -191,6 +194,18 @@ __device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, 
     const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int32_t total = a.batch ? cn[a.batch] : 0;
     if (tid == 0 && total > a.rows) flag(a.status, IX_DEV_BAD_RANGE);
+    // the new blocks' table entries, a request to a warp: no row reads them.  (The
+    // last warps first: they have fewer rows.)
+    for (int64_t b = (threads - 1 - tid) / 32; b < a.batch; b += threads / 32) {
+        const int32_t have = static_cast<int32_t>(blocks_of(a, max(__ldg(a.cached + b), 0)));
+        const int64_t first = cb[b], lack = cb[b + 1] - first;
+        for (int64_t k = threadIdx.x & 31; k < lack; k += 32) {
+            if (have + k < a.width)
+                a.table[b * a.stride + have + k] = free_block(a, first + k);
+            else
+                flag(a.status, IX_DEV_BAD_RANGE);
+        }
+    }
     for (int64_t t0 = tid * kRows; t0 < a.rows; t0 += threads * kRows) {
         int64_t slot[kRows], pos[kRows];
         int32_t req[kRows], len[kRows], lo[kRows], hi[kRows];
@@ -253,17 +268,6 @@ __device__ void expand(const PlanArgs& a, const int32_t* cn, const int32_t* cc, 
                 }
             }
         }
-    }
-    // the new blocks' table entries: no row above reads them
-    const int32_t taken = a.batch ? cb[a.batch] : 0;
-    // (the last threads first: in a small step they have no rows)
-    for (int64_t k = threads - 1 - tid; k < taken; k += threads) {
-        const int b = find_request(cb, a.batch, static_cast<int32_t>(k));
-        const int64_t j = static_cast<int64_t>(blocks_of(a, max(__ldg(a.cached + b), 0))) + (k - cb[b]);
-        if (j < a.width)
-            a.table[b * a.stride + j] = free_block(a, k);
-        else
-            flag(a.status, IX_DEV_BAD_RANGE);
     }
 }
 
