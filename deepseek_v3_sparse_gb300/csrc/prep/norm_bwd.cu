@@ -13,7 +13,7 @@
 // an SM, 63 us; CTAs of 512 threads 45.5 us; h and xhat kept and mean and rstd copied ahead with
 // their row (loaded by each thread they came late) 37.6 us.  Beyond 4096 columns a
 // CTA has one row and waits for its sums: 4099 x 5001 f32, whose vectors are cut
-// besides, 49.7 us (73%).
+// besides, 49.4 us (74%).  Few rows cost two launches: 99 x 4096 bf16 6.8 us.
 #include "norm.cuh"
 
 namespace dsix {
@@ -54,7 +54,8 @@ struct Bwd : RowShape<G, 512> {
     static constexpr int stages = (kRowSmem - gamma_smem) / row < 4 ? (kRowSmem - gamma_smem) / row : 4;
     static constexpr bool async = bytes >= 4 && stages > 0;
     // the CTA's column sums of one weight, row by row, take the rows' place in the end
-    static constexpr int cols = G * E, sums_smem = Shape::rows * cols * static_cast<int>(sizeof(float));
+    // (a column in 32 is left out: threads whose columns lie V apart meet no bank twice)
+    static constexpr int cols = G * E + G * E / 32, sums_smem = Shape::rows * cols * static_cast<int>(sizeof(float));
     static constexpr int rows_smem = async ? stages * row : 0;
     static constexpr int smem = rows_smem + gamma_smem < sums_smem ? sums_smem : rows_smem + gamma_smem;
 };
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
         for (int u = 0; u < U; ++u) weight(u, u);
     }
     if constexpr (F::gamma_near) {
-#pragma unroll 1
+#pragma unroll
         for (int u = 0; u < U; ++u) {
             float w[V];
             load_weight<T, V, kShift>(a.gamma, a.weight_f32, c0 + u * G * V, a.cols, 1.f, w);
@@ -275,22 +276,15 @@ __global__ void __launch_bounds__(Bwd<T, V, G, U>::threads) norm_bwd_kernel(cons
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + u * G * V;
                 const float* v = (w ? ab : ag) + u * V;
-                if constexpr (!kShift && V % 4 == 0) {
 #pragma unroll
-                    for (int i = 0; i < V; i += 4)
-                        *reinterpret_cast<float4*>(s_part + sub * F::cols + c + i) =
-                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (c + i >= 0) s_part[sub * F::cols + c + i] = v[i];
-                }
+                for (int i = 0; i < V; ++i)
+                    if (!kShift || c + i >= 0) s_part[sub * F::cols + c + i + ((c + i) >> 5)] = v[i];
             }
             __syncthreads();
             for (int c = threadIdx.x; c < a.cols; c += F::threads) {
                 float v = 0.f;
 #pragma unroll 8
-                for (int k = 0; k < F::Shape::rows; ++k) v += s_part[k * F::cols + c];
+                for (int k = 0; k < F::Shape::rows; ++k) v += s_part[k * F::cols + c + (c >> 5)];
                 part[w * a.cols + c] = v;
             }
         }
