@@ -10,10 +10,12 @@
 // Bound by DRAM up to 8192 columns: 8192 x 4096 bf16 in 36.7 us, 5.5 TB/s, 81% of a
 // copy's rate; 131071 x 128 bf16 in 20.1 us (75%), of which the second kernel is
 // about 2 us.  What it took, at 8192 x 4096: CTAs of one row and 128 threads, two to
-// an SM, 63 us; CTAs of 512 threads 45.5 us; h and xhat kept and mean and rstd copied ahead with
-// their row (loaded by each thread they came late) 37.6 us.  Beyond 4096 columns a
-// CTA has one row and waits for its sums: 4099 x 5001 f32, whose vectors are cut
-// besides, 49.4 us (74%).  Few rows cost two launches: 99 x 4096 bf16 6.8 us.
+// an SM, 63 us; CTAs of 512 threads 45.5 us; h and xhat kept, and mean and rstd copied
+// ahead with their row (loaded by each thread they came late) 37.6 us.  Beyond 4096
+// columns a CTA has one row, whose passes follow one another: 4099 x 5001 f32, whose
+// vectors are cut besides, 49.4 us (74%); taking the next row's first pass before the
+// second of this one changed nothing.  Few rows cost two launches: 99 x 4096 bf16
+// 6.8 us.
 #include "norm.cuh"
 
 namespace dsix {
