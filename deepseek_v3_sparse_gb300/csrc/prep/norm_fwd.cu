@@ -190,7 +190,7 @@ int launch(const NormArgs& a, cudaStream_t s) {
     return launch_status();
 }
 
-// 32 elements a thread, fewer where the row is short
+// 32 elements a thread, or 24, fewer where the row is short
 template <class T, bool kShift>
 int by_width(const NormArgs& a, cudaStream_t s) {
     constexpr int W = 16 / sizeof(T), U = 32 / W;
@@ -198,11 +198,17 @@ int by_width(const NormArgs& a, cudaStream_t s) {
     if (n <= 64) return launch<T, W, 8, U / 4, kShift>(a, s);
     if (n <= 128) return launch<T, W, 8, U / 2, kShift>(a, s);
     if (n <= 256) return launch<T, W, 8, U, kShift>(a, s);
+    if (n <= 384) return launch<T, W, 16, 3 * U / 4, kShift>(a, s);
     if (n <= 512) return launch<T, W, 16, U, kShift>(a, s);
+    if (n <= 768) return launch<T, W, 32, 3 * U / 4, kShift>(a, s);
     if (n <= 1024) return launch<T, W, 32, U, kShift>(a, s);
+    if (n <= 1536) return launch<T, W, 64, 3 * U / 4, kShift>(a, s);
     if (n <= 2048) return launch<T, W, 64, U, kShift>(a, s);
+    if (n <= 3072) return launch<T, W, 128, 3 * U / 4, kShift>(a, s);
     if (n <= 4096) return launch<T, W, 128, U, kShift>(a, s);
+    if (n <= 6144) return launch<T, W, 256, 3 * U / 4, kShift>(a, s);
     if (n <= 8192) return launch<T, W, 256, U, kShift>(a, s);
+    if (n <= 12288) return launch<T, W, 512, 3 * U / 4, kShift>(a, s);
     if (n <= 16384) return launch<T, W, 512, U, kShift>(a, s);
     return launch<T, W, 1024, U + (kShift ? 1 : 0), kShift>(a, s);
 }
